@@ -1,0 +1,130 @@
+/*
+ * trsm_model.h -- C ABI of the operators for recurrent sequence models and
+ *                 their training (libtrsm_gb300.so).
+ *
+ * Two operations stand next to the triangular solves of trsm.h:
+ *
+ *  - the gated linear recurrence, one per channel of a sequence,
+ *
+ *        h_t = a_t h_{t-1} + u_t,      t = 0 .. T-1,
+ *
+ *    which is the solve of a unit lower bidiagonal system (ones on the
+ *    diagonal, -a_t below it); its backward pass is the solve with the
+ *    transposed matrix;
+ *  - the orthogonalisation of an update matrix by Newton-Schulz products,
+ *    which brings the singular values of a matrix towards one without a
+ *    factorisation.
+ *
+ * Conventions: those of trsm.h (DEVICE pointers owned by the caller, strides
+ * in ELEMENTS, stream-ordered and asynchronous, -k for the first invalid
+ * argument, TRSM_ERR_CUDA_BASE + cudaError_t for a CUDA error, quick returns
+ * that touch no memory).  Outputs must not overlap inputs or each other
+ * unless an entry says so.  Pointers are aligned to their element; strides
+ * and alignments that are multiples of 16 bytes run faster.
+ */
+#ifndef TRSM_MODEL_GB300_H
+#define TRSM_MODEL_GB300_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* element types of these operators: float, IEEE half, bfloat16 */
+typedef enum { TRSM_ELEM_F32 = 0, TRSM_ELEM_F16 = 1, TRSM_ELEM_BF16 = 2 } trsm_elem_t;
+
+/*
+ * What the gate values g say:
+ *   TRSM_GATE_DECAY    a = g,           u = x
+ *   TRSM_GATE_LOG      a = exp(g),      u = x
+ *   TRSM_GATE_SIGMOID  a = sigmoid(g),  u = (1 - a) x
+ * The decay itself has few values near one in 16 bits (bfloat16: none between
+ * 0.99609375 and 1); the other two forms keep long memories apart.
+ */
+typedef enum { TRSM_GATE_DECAY = 0, TRSM_GATE_LOG = 1, TRSM_GATE_SIGMOID = 2 } trsm_gate_t;
+
+/*
+ * Forward recurrence over `batch` sequences of `T` tokens and `D` channels.
+ *
+ * gate, x (inputs) and h (output) hold element (b, t, d) at
+ * b*stride_b + t*stride_t + d; any strides are accepted for the inputs, also
+ * 0; h's rows must be disjoint.  h0: the initial states, float, (b, d) at
+ * b*h0_stride + d, or NULL for zero.  h_last: receives the last states,
+ * float, (b, d) at b*D + d, or NULL; a sequence without tokens has h0 there.
+ *
+ * offsets != NULL: packed sequences.  gate, x and h are lists of T rows (the
+ * stride_b arguments are not used), offsets a device array of batch + 1
+ * row numbers, and sequence b is rows offsets[b] .. offsets[b+1] - 1; it may
+ * be empty.  Row numbers outside 0 .. T are taken as the nearest inside and a
+ * decreasing pair as an empty sequence; rows of no sequence are not written.
+ *
+ * The states are carried in float along a sequence whatever the element
+ * type; h holds them rounded to it.  T is at most 2^31 - 2^16.
+ *
+ * Arguments: 1 dtype, 2 form, 3 batch, 4 T, 5 D, 6 gate, 7 gate_stride_b,
+ * 8 gate_stride_t, 9 x, 10 x_stride_b, 11 x_stride_t, 12 h0, 13 h0_stride,
+ * 14 offsets, 15 h, 16 h_stride_b, 17 h_stride_t, 18 h_last, 19 stream.
+ */
+int trsm_linrec_forward(trsm_elem_t dtype, trsm_gate_t form, int64_t batch, int64_t T, int64_t D, const void *gate,
+                        int64_t gate_stride_b, int64_t gate_stride_t, const void *x, int64_t x_stride_b,
+                        int64_t x_stride_t, const float *h0, int64_t h0_stride, const int32_t *offsets, void *h,
+                        int64_t h_stride_b, int64_t h_stride_t, float *h_last, void *stream);
+
+/*
+ * Backward pass: from dh (the gradient of h) and dh_last (that of h_last,
+ * float, (b, d) at b*D + d, or NULL for zero) to dgate, dx (of the element
+ * type) and dh0 (float, (b, d) at b*D + d, or NULL).  With D_t the gradient
+ * of the state h_t including what later tokens pass back,
+ *
+ *     D_t = dh_t + a_{t+1} D_{t+1}   (D_{T-1} = dh_{T-1} + dh_last)
+ *     decay:    dgate = D_t h_{t-1},               dx = D_t
+ *     log:      dgate = D_t h_{t-1} a_t,           dx = D_t
+ *     sigmoid:  dgate = D_t (h_{t-1} - x_t) a_t (1 - a_t),  dx = D_t (1 - a_t)
+ *     dh0 = a_0 D_0
+ *
+ * h holds the forward pass's output; h_{-1} is h0.  x is read in the sigmoid
+ * form only and may be NULL in the others.  gate, x, h, dh, dgate and dx are
+ * laid out as in trsm_linrec_forward, each with its own strides.
+ *
+ * Arguments: 1 dtype, 2 form, 3 batch, 4 T, 5 D, 6 gate, 7 gate_stride_b,
+ * 8 gate_stride_t, 9 x, 10 x_stride_b, 11 x_stride_t, 12 h, 13 h_stride_b,
+ * 14 h_stride_t, 15 h0, 16 h0_stride, 17 dh, 18 dh_stride_b, 19 dh_stride_t,
+ * 20 dh_last, 21 offsets, 22 dgate, 23 dgate_stride_b, 24 dgate_stride_t,
+ * 25 dx, 26 dx_stride_b, 27 dx_stride_t, 28 dh0, 29 stream.
+ */
+int trsm_linrec_backward(trsm_elem_t dtype, trsm_gate_t form, int64_t batch, int64_t T, int64_t D, const void *gate,
+                         int64_t gate_stride_b, int64_t gate_stride_t, const void *x, int64_t x_stride_b,
+                         int64_t x_stride_t, const void *h, int64_t h_stride_b, int64_t h_stride_t, const float *h0,
+                         int64_t h0_stride, const void *dh, int64_t dh_stride_b, int64_t dh_stride_t,
+                         const float *dh_last, const int32_t *offsets, void *dgate, int64_t dgate_stride_b,
+                         int64_t dgate_stride_t, void *dx, int64_t dx_stride_b, int64_t dx_stride_t, float *dh0,
+                         void *stream);
+
+/*
+ * One token for each of `batch` sequences, out of a table of states: with
+ * s = slots[i] (slots == NULL: s = i),
+ *
+ *     y_i = next[s] = a_i state[s] + u_i.
+ *
+ * gate, x, y: row i at i*stride, D elements.  state, next: float, row s at
+ * s*stride, nslots rows; next may be state itself (update in place) and gets
+ * no row that is not named.  A slot outside 0 .. nslots - 1 marks a row
+ * without a sequence (padding): its y is set to zero and no state is read or
+ * written.  A slot named twice has an undefined next state.
+ *
+ * Arguments: 1 dtype, 2 form, 3 batch, 4 D, 5 gate, 6 gate_stride, 7 x,
+ * 8 x_stride, 9 slots, 10 nslots, 11 state, 12 state_stride, 13 next,
+ * 14 next_stride, 15 y, 16 y_stride, 17 stream.
+ */
+int trsm_linrec_step(trsm_elem_t dtype, trsm_gate_t form, int64_t batch, int64_t D, const void *gate,
+                     int64_t gate_stride, const void *x, int64_t x_stride, const int32_t *slots, int64_t nslots,
+                     const float *state, int64_t state_stride, float *next, int64_t next_stride, void *y,
+                     int64_t y_stride, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* TRSM_MODEL_GB300_H */

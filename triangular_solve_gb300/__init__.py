@@ -24,6 +24,8 @@ __all__ = [
     "trsm_status_string", "trsm_llnn_noalloc", "trsm_device_status", "trsm_set_wait_limit",
     "solve", "TrsmError",
     "library_path", "load_library",
+    "trsm_linrec_forward", "trsm_linrec_backward", "trsm_linrec_step",
+    "linear_recurrence", "linear_recurrence_backward", "linear_recurrence_step",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -328,3 +330,9 @@ def solve(A, B, alpha=1.0, stream=None):
     sb = B.stride(0) if batched else 0
     trsm_llnn_strided_batched(code, lb, m, n, alpha, A, lda, sa, B, ldb, sb, batch, stream)
     return B
+
+
+# the operators of include/trsm_model.h
+from .model import (  # noqa: E402
+    linear_recurrence, linear_recurrence_backward, linear_recurrence_step, trsm_linrec_backward,
+    trsm_linrec_forward, trsm_linrec_step)

@@ -1,0 +1,48 @@
+// Internal interface of the gated linear recurrence (trsm_linrec_*): the
+// arguments of the kernels and their launchers, one translation unit per
+// element type.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace trsm {
+
+// A tensor of rows: element (b, t, d) at p + b*sb + t*st + d.
+struct LinrecRows {
+    const void *p;
+    int64_t sb, st;
+};
+struct LinrecArgs {
+    int64_t batch, T, D;
+    LinrecRows gate, x;     // both directions (x: backward only in the sigmoid form)
+    LinrecRows h;           // forward: the output; backward: the forward pass's output
+    LinrecRows dh;          // backward
+    LinrecRows dgate, dx;   // backward, outputs
+    const float *h0;        // may be null
+    int64_t h0_stride;
+    const float *dh_last;   // backward, may be null
+    float *last;            // forward: h_last, backward: dh0; may be null
+    const int32_t *offsets; // packed sequences, may be null
+};
+
+struct LinrecStepArgs {
+    int64_t batch, D, nslots;
+    const void *gate, *x;
+    int64_t gate_stride, x_stride;
+    const int32_t *slots;  // may be null
+    const float *state;
+    float *next;
+    int64_t state_stride, next_stride;
+    void *y;
+    int64_t y_stride;
+};
+
+int linrec_run_f32(const LinrecArgs &a, int form, bool backward, cudaStream_t st);
+int linrec_run_f16(const LinrecArgs &a, int form, bool backward, cudaStream_t st);
+int linrec_run_bf16(const LinrecArgs &a, int form, bool backward, cudaStream_t st);
+int linrec_step_f32(const LinrecStepArgs &a, int form, cudaStream_t st);
+int linrec_step_f16(const LinrecStepArgs &a, int form, cudaStream_t st);
+int linrec_step_bf16(const LinrecStepArgs &a, int form, cudaStream_t st);
+
+}  // namespace trsm

@@ -1,0 +1,159 @@
+// C ABI of the operators of trsm_model.h: argument checking and dispatch.
+#include <stdint.h>
+
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "linrec.h"
+#include "trsm_model.h"
+
+using namespace trsm;
+
+namespace {
+
+int64_t elem_size(int dtype) {
+    switch (dtype) {
+        case TRSM_ELEM_F32: return 4;
+        case TRSM_ELEM_F16:
+        case TRSM_ELEM_BF16: return 2;
+        default: return 0;
+    }
+}
+
+bool good(const void *p, int64_t align) { return p && reinterpret_cast<uintptr_t>(p) % (uintptr_t)align == 0; }
+bool good_or_null(const void *p, int64_t align) { return !p || good(p, align); }
+
+bool known_form(int form) { return form == TRSM_GATE_DECAY || form == TRSM_GATE_LOG || form == TRSM_GATE_SIGMOID; }
+
+constexpr int64_t kMaxT = 0x7fff0000;  // positions are counted in int
+
+// Output rows: each D long, disjoint (packed: one list of rows).
+int64_t magnitude(int64_t v) { return v < 0 ? -v : v; }
+bool rows_disjoint(int64_t rows, int64_t D, int64_t st) { return rows <= 1 || magnitude(st) >= D; }
+
+int run(int dtype, const LinrecArgs &a, int form, bool backward, cudaStream_t st) {
+    switch (dtype) {
+        case TRSM_ELEM_F32: return linrec_run_f32(a, form, backward, st);
+        case TRSM_ELEM_F16: return linrec_run_f16(a, form, backward, st);
+        default: return linrec_run_bf16(a, form, backward, st);
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+int trsm_linrec_forward(trsm_elem_t dtype, trsm_gate_t form, int64_t batch, int64_t T, int64_t D, const void *gate,
+                        int64_t gate_stride_b, int64_t gate_stride_t, const void *x, int64_t x_stride_b,
+                        int64_t x_stride_t, const float *h0, int64_t h0_stride, const int32_t *offsets, void *h,
+                        int64_t h_stride_b, int64_t h_stride_t, float *h_last, void *stream) {
+    const int64_t es = elem_size((int)dtype);
+    if (!es) return -1;
+    if (!known_form((int)form)) return -2;
+    if (batch < 0) return -3;
+    if (T < 0 || T > kMaxT) return -4;
+    if (D < 0) return -5;
+    if (batch == 0 || D == 0) return TRSM_SUCCESS;
+    const bool empty = T == 0;  // h_last still receives h0
+    if (!empty && !good(gate, es)) return -6;
+    if (!empty && !good(x, es)) return -9;
+    if (!good_or_null(h0, 4)) return -12;
+    if (!good_or_null(offsets, 4)) return -14;
+    if (!empty && !good(h, es)) return -15;
+    if (!offsets && !rows_disjoint(batch, D, h_stride_b)) return -16;
+    if (!rows_disjoint(T, D, h_stride_t)) return -17;
+    if (!good_or_null(h_last, 4)) return -18;
+    if (empty && !h_last) return TRSM_SUCCESS;
+    LinrecArgs a = {};
+    a.batch = batch;
+    a.T = T;
+    a.D = D;
+    a.gate = {gate, gate_stride_b, gate_stride_t};
+    a.x = {x, x_stride_b, x_stride_t};
+    a.h = {h, h_stride_b, h_stride_t};
+    a.h0 = h0;
+    a.h0_stride = h0_stride;
+    a.last = h_last;
+    a.offsets = offsets;
+    return run((int)dtype, a, (int)form, false, static_cast<cudaStream_t>(stream));
+}
+
+int trsm_linrec_backward(trsm_elem_t dtype, trsm_gate_t form, int64_t batch, int64_t T, int64_t D, const void *gate,
+                         int64_t gate_stride_b, int64_t gate_stride_t, const void *x, int64_t x_stride_b,
+                         int64_t x_stride_t, const void *h, int64_t h_stride_b, int64_t h_stride_t, const float *h0,
+                         int64_t h0_stride, const void *dh, int64_t dh_stride_b, int64_t dh_stride_t,
+                         const float *dh_last, const int32_t *offsets, void *dgate, int64_t dgate_stride_b,
+                         int64_t dgate_stride_t, void *dx, int64_t dx_stride_b, int64_t dx_stride_t, float *dh0,
+                         void *stream) {
+    const int64_t es = elem_size((int)dtype);
+    if (!es) return -1;
+    if (!known_form((int)form)) return -2;
+    if (batch < 0) return -3;
+    if (T < 0 || T > kMaxT) return -4;
+    if (D < 0) return -5;
+    if (batch == 0 || D == 0) return TRSM_SUCCESS;
+    const bool empty = T == 0;  // dh0 still receives dh_last
+    if (!empty && !good(gate, es)) return -6;
+    if (!empty && (form == TRSM_GATE_SIGMOID ? !good(x, es) : !good_or_null(x, es))) return -9;
+    if (!empty && !good(h, es)) return -12;
+    if (!good_or_null(h0, 4)) return -15;
+    if (!empty && !good(dh, es)) return -17;
+    if (!good_or_null(dh_last, 4)) return -20;
+    if (!good_or_null(offsets, 4)) return -21;
+    if (!empty && !good(dgate, es)) return -22;
+    if (!offsets && !rows_disjoint(batch, D, dgate_stride_b)) return -23;
+    if (!rows_disjoint(T, D, dgate_stride_t)) return -24;
+    if (!empty && !good(dx, es)) return -25;
+    if (!offsets && !rows_disjoint(batch, D, dx_stride_b)) return -26;
+    if (!rows_disjoint(T, D, dx_stride_t)) return -27;
+    if (!good_or_null(dh0, 4)) return -28;
+    if (empty && !dh0) return TRSM_SUCCESS;
+    LinrecArgs a = {};
+    a.batch = batch;
+    a.T = T;
+    a.D = D;
+    a.gate = {gate, gate_stride_b, gate_stride_t};
+    a.x = {x, x_stride_b, x_stride_t};
+    a.h = {h, h_stride_b, h_stride_t};
+    a.dh = {dh, dh_stride_b, dh_stride_t};
+    a.dgate = {dgate, dgate_stride_b, dgate_stride_t};
+    a.dx = {dx, dx_stride_b, dx_stride_t};
+    a.h0 = h0;
+    a.h0_stride = h0_stride;
+    a.dh_last = dh_last;
+    a.last = dh0;
+    a.offsets = offsets;
+    return run((int)dtype, a, (int)form, true, static_cast<cudaStream_t>(stream));
+}
+
+int trsm_linrec_step(trsm_elem_t dtype, trsm_gate_t form, int64_t batch, int64_t D, const void *gate,
+                     int64_t gate_stride, const void *x, int64_t x_stride, const int32_t *slots, int64_t nslots,
+                     const float *state, int64_t state_stride, float *next, int64_t next_stride, void *y,
+                     int64_t y_stride, void *stream) {
+    const int64_t es = elem_size((int)dtype);
+    if (!es) return -1;
+    if (!known_form((int)form)) return -2;
+    if (batch < 0) return -3;
+    if (D < 0) return -4;
+    if (batch == 0 || D == 0) return TRSM_SUCCESS;
+    if (!good(gate, es)) return -5;
+    if (!good(x, es)) return -7;
+    if (!good_or_null(slots, 4)) return -9;
+    if (nslots < 0) return -10;
+    if (nslots && !good(state, 4)) return -11;
+    if (!rows_disjoint(nslots, D, state_stride)) return -12;
+    if (nslots && !good(next, 4)) return -13;
+    if (!rows_disjoint(nslots, D, next_stride)) return -14;
+    if (!good(y, es)) return -15;
+    if (!rows_disjoint(batch, D, y_stride)) return -16;
+    const LinrecStepArgs a = {batch, D, nslots, gate, x, gate_stride, x_stride, slots, state, next,
+                              state_stride, next_stride, y, y_stride};
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    switch ((int)dtype) {
+        case TRSM_ELEM_F32: return linrec_step_f32(a, (int)form, st);
+        case TRSM_ELEM_F16: return linrec_step_f16(a, (int)form, st);
+        default: return linrec_step_bf16(a, (int)form, st);
+    }
+}
+
+}  // extern "C"

@@ -1,0 +1,294 @@
+"""Python binding of the operators of ``include/trsm_model.h``: the gated
+linear recurrence (forward, backward, single tokens) of recurrent sequence
+models, next to the triangular solves it is a special case of.
+
+``trsm_linrec_*`` mirror the C ABI one to one.  ``linear_recurrence`` (which
+is differentiable), ``linear_recurrence_backward`` and
+``linear_recurrence_step`` take torch tensors, check them, allocate the
+outputs and run on the tensors' device and torch's current stream.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import _check, _ptr, _stream, load_library
+
+ELEMS = {"f32": 0, "f16": 1, "bf16": 2}
+FORMS = {"decay": 0, "log": 1, "sigmoid": 2}
+
+_typed = None
+
+
+def _library():
+    """The loaded library, with the types of trsm_model.h's entry points."""
+    global _typed
+    if _typed is None:
+        lib = load_library()
+        i32, i64, vp = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p
+        rows = [vp, i64, i64]
+        lib.trsm_linrec_forward.argtypes = [i32, i32, i64, i64, i64, *rows, *rows, vp, i64, vp, *rows, vp, vp]
+        lib.trsm_linrec_backward.argtypes = [i32, i32, i64, i64, i64, *rows, *rows, *rows, vp, i64, *rows, vp, vp,
+                                             *rows, *rows, vp, vp]
+        lib.trsm_linrec_step.argtypes = [i32, i32, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+        for fn in (lib.trsm_linrec_forward, lib.trsm_linrec_backward, lib.trsm_linrec_step):
+            fn.restype = i32
+        _typed = lib
+    return _typed
+
+
+def _code(table, v, what):
+    if isinstance(v, str) and v in table:
+        return table[v]
+    if isinstance(v, int) and v in table.values():
+        return v
+    raise ValueError(f"{what}: {v!r} (one of {', '.join(table)})")
+
+
+# ------------------------------------------------------------------ C ABI mirror
+def trsm_linrec_forward(dtype, form, batch, T, D, gate, gate_stride_b, gate_stride_t, x, x_stride_b, x_stride_t, h0,
+                        h0_stride, offsets, h, h_stride_b, h_stride_t, h_last, stream=None) -> None:
+    """h_t = a_t h_{t-1} + u_t over `batch` sequences (see include/trsm_model.h)."""
+    _check("trsm_linrec_forward", _library().trsm_linrec_forward(
+        _code(ELEMS, dtype, "dtype"), _code(FORMS, form, "form"), batch, T, D, _ptr(gate), gate_stride_b,
+        gate_stride_t, _ptr(x), x_stride_b, x_stride_t, _ptr(h0), h0_stride, _ptr(offsets), _ptr(h), h_stride_b,
+        h_stride_t, _ptr(h_last), _stream(stream)))
+
+
+def trsm_linrec_backward(dtype, form, batch, T, D, gate, gate_stride_b, gate_stride_t, x, x_stride_b, x_stride_t, h,
+                         h_stride_b, h_stride_t, h0, h0_stride, dh, dh_stride_b, dh_stride_t, dh_last, offsets, dgate,
+                         dgate_stride_b, dgate_stride_t, dx, dx_stride_b, dx_stride_t, dh0, stream=None) -> None:
+    """The recurrence's backward pass (see include/trsm_model.h)."""
+    _check("trsm_linrec_backward", _library().trsm_linrec_backward(
+        _code(ELEMS, dtype, "dtype"), _code(FORMS, form, "form"), batch, T, D, _ptr(gate), gate_stride_b,
+        gate_stride_t, _ptr(x), x_stride_b, x_stride_t, _ptr(h), h_stride_b, h_stride_t, _ptr(h0), h0_stride, _ptr(dh),
+        dh_stride_b, dh_stride_t, _ptr(dh_last), _ptr(offsets), _ptr(dgate), dgate_stride_b, dgate_stride_t, _ptr(dx),
+        dx_stride_b, dx_stride_t, _ptr(dh0), _stream(stream)))
+
+
+def trsm_linrec_step(dtype, form, batch, D, gate, gate_stride, x, x_stride, slots, nslots, state, state_stride, next,
+                     next_stride, y, y_stride, stream=None) -> None:
+    """One token per row over a table of states (see include/trsm_model.h)."""
+    _check("trsm_linrec_step", _library().trsm_linrec_step(
+        _code(ELEMS, dtype, "dtype"), _code(FORMS, form, "form"), batch, D, _ptr(gate), gate_stride, _ptr(x), x_stride,
+        _ptr(slots), nslots, _ptr(state), state_stride, _ptr(next), next_stride, _ptr(y), y_stride, _stream(stream)))
+
+
+# ------------------------------------------------------------------ torch tensors
+_torch = None
+_elem = {}
+
+
+def _load_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _elem.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+        _torch = torch
+    return _torch
+
+
+def _on_device(t, launch):
+    """Runs launch(stream) with t's device current, on its current stream."""
+    cuda = _torch.cuda
+    if t.get_device() == cuda.current_device():
+        return launch(cuda.current_stream().cuda_stream)
+    with cuda.device(t.device):
+        return launch(cuda.current_stream().cuda_stream)
+
+
+def _rows(name, t, like):
+    """A tensor of `like`'s shape, type and device with contiguous channels."""
+    if t.shape != like.shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name}: {t.dtype}, expected {like.dtype}")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{name}: on {t.device}, expected {like.device}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
+        raise ValueError(f"{name}: the channels (last dimension) must be contiguous")
+
+
+def _float_state(name, t, shape, like):
+    if t.dtype != _torch.float32:
+        raise TypeError(f"{name}: states are float32, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{name}: on {t.device}, expected {like.device}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
+        raise ValueError(f"{name}: the channels (last dimension) must be contiguous")
+
+
+def _geometry(gate, offsets):
+    """(element code, batch, T, D) of batched or packed sequences."""
+    if not gate.is_cuda:
+        raise ValueError("the recurrence takes CUDA (device) tensors; got a CPU tensor")
+    code = _elem.get(gate.dtype)
+    if code is None:
+        raise TypeError(f"gate: {gate.dtype} (float32, float16 or bfloat16)")
+    if gate.stride(-1) != 1 and gate.shape[-1] > 1 and gate.numel():
+        raise ValueError("gate: the channels (last dimension) must be contiguous")
+    if offsets is None:
+        if gate.dim() != 3:
+            raise ValueError("gate: expected (batch, T, D), or (rows, D) with offsets")
+        return code, gate.shape[0], gate.shape[1], gate.shape[2]
+    if gate.dim() != 2:
+        raise ValueError("gate: packed sequences (offsets) are (rows, D)")
+    if offsets.dtype != _torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_contiguous():
+        raise ValueError("offsets: a contiguous int32 vector of batch + 1 row numbers")
+    if offsets.get_device() != gate.get_device():
+        raise ValueError(f"offsets: on {offsets.device}, expected {gate.device}")
+    return code, offsets.shape[0] - 1, gate.shape[0], gate.shape[1]
+
+
+def _strides(t):
+    """(pointer, stride_b, stride_t) of a batched or packed tensor."""
+    if t.dim() == 3:
+        return t.data_ptr(), t.stride(0), t.stride(1)
+    return t.data_ptr(), 0, t.stride(0)
+
+
+def _pointer(t):
+    return None if t is None else t.data_ptr()
+
+
+def _forward(gate, x, h0, form, offsets):
+    torch = _load_torch()
+    code, batch, T, D = _geometry(gate, offsets)
+    kind = _code(FORMS, form, "form")
+    _rows("x", x, gate)
+    if h0 is not None:
+        _float_state("h0", h0, (batch, D), gate)
+    h = torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
+    last = torch.empty((batch, D), dtype=torch.float32, device=gate.device)
+    _check("trsm_linrec_forward", _on_device(gate, lambda st: _library().trsm_linrec_forward(
+        code, kind, batch, T, D, *_strides(gate), *_strides(x), _pointer(h0), 0 if h0 is None else h0.stride(0),
+        _pointer(offsets), *_strides(h), last.data_ptr(), st)))
+    return h, last
+
+
+def linear_recurrence_backward(gate, x, h, dh, h0=None, dh_last=None, *, form="decay", offsets=None):
+    """Gradients (dgate, dx, dh0) of ``linear_recurrence`` from ``h``, its
+    output, and ``dh`` and ``dh_last``, the gradients of its two results
+    (dh_last None: zero).  ``x`` may be None unless form is "sigmoid"."""
+    torch = _load_torch()
+    code, batch, T, D = _geometry(gate, offsets)
+    kind = _code(FORMS, form, "form")
+    if x is not None:
+        _rows("x", x, gate)
+    elif kind == FORMS["sigmoid"]:
+        raise ValueError("x: needed by the sigmoid form")
+    _rows("h", h, gate)
+    _rows("dh", dh, gate)
+    if h0 is not None:
+        _float_state("h0", h0, (batch, D), gate)
+    if dh_last is not None:
+        _float_state("dh_last", dh_last, (batch, D), gate)
+        if not dh_last.is_contiguous():
+            dh_last = dh_last.contiguous()
+    dgate = torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
+    dx = torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
+    dh0 = torch.empty((batch, D), dtype=torch.float32, device=gate.device)
+    _check("trsm_linrec_backward", _on_device(gate, lambda st: _library().trsm_linrec_backward(
+        code, kind, batch, T, D, *_strides(gate), *((None, 0, 0) if x is None else _strides(x)), *_strides(h),
+        _pointer(h0), 0 if h0 is None else h0.stride(0), *_strides(dh), _pointer(dh_last), _pointer(offsets),
+        *_strides(dgate), *_strides(dx), dh0.data_ptr(), st)))
+    return dgate, dx, dh0
+
+
+_function = None
+
+
+def _autograd():
+    """The recurrence as a torch.autograd.Function (made on first use: this
+    package does not import torch by itself)."""
+    global _function
+    if _function is None:
+        torch = _load_torch()
+        from torch.autograd.function import once_differentiable
+
+        class LinearRecurrence(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, gate, x, h0, form, offsets):
+                h, last = _forward(gate, x, h0, form, offsets)
+                ctx.set_materialize_grads(False)
+                ctx.form = form
+                ctx.save_for_backward(gate, x if _code(FORMS, form, "form") == FORMS["sigmoid"] else None, h, h0,
+                                      offsets)
+                return h, last
+
+            @staticmethod
+            @once_differentiable
+            def backward(ctx, dh, dlast):
+                gate, x, h, h0, offsets = ctx.saved_tensors
+                if dh is None:
+                    dh = torch.zeros_like(h)
+                elif dh.stride(-1) != 1:
+                    dh = dh.contiguous()  # a broadcast gradient, as of a sum
+                if dlast is not None and dlast.stride(-1) != 1:
+                    dlast = dlast.contiguous()
+                dgate, dx, dh0 = linear_recurrence_backward(gate, x, h, dh, h0, dlast, form=ctx.form, offsets=offsets)
+                return dgate, dx, dh0 if h0 is not None else None, None, None
+
+        _function = LinearRecurrence
+    return _function
+
+
+def linear_recurrence(gate, x, h0=None, *, form="decay", offsets=None):
+    """The gated linear recurrence h_t = a_t h_{t-1} + u_t per channel.
+
+    ``gate`` and ``x`` are CUDA tensors (batch, T, D) of float32, float16 or
+    bfloat16 with contiguous channels and any other strides (halves of one
+    projection, for example).  ``form`` says what the gate holds: "decay" (a =
+    gate, u = x), "log" (a = exp(gate), u = x) or "sigmoid" (a =
+    sigmoid(gate), u = (1 - a) x).  ``h0`` (batch, D) float32 is the state
+    before the first token, zero if None.  With ``offsets`` (batch + 1 row
+    numbers, int32) the tensors are packed sequences (rows, D).
+
+    Returns (h, h_last): all states, of gate's type, and the last ones in
+    float32.  Differentiable in gate, x and h0.
+    """
+    torch = _load_torch()
+    if torch.is_grad_enabled() and (gate.requires_grad or x.requires_grad or (h0 is not None and h0.requires_grad)):
+        return _autograd().apply(gate, x, h0, form, offsets)
+    return _forward(gate, x, h0, form, offsets)
+
+
+def linear_recurrence_step(gate, x, state, *, form="decay", slots=None, out_state=None):
+    """One token of ``linear_recurrence`` for each row of ``gate`` and ``x``
+    (batch, D), out of a table of float32 states (slots, D): row i takes the
+    state ``slots[i]`` (int32; None: row i's own) and leaves the next one
+    there, in ``out_state`` where given (rows not named stay as they are),
+    else in ``state`` itself.  A slot outside the table marks a row of
+    padding: zero comes out and no state is touched.  Returns the new states
+    as (batch, D) of gate's type."""
+    torch = _load_torch()
+    if not gate.is_cuda:
+        raise ValueError("the recurrence takes CUDA (device) tensors; got a CPU tensor")
+    code = _elem.get(gate.dtype)
+    if code is None:
+        raise TypeError(f"gate: {gate.dtype} (float32, float16 or bfloat16)")
+    if gate.dim() != 2:
+        raise ValueError("gate: expected (batch, D)")
+    kind = _code(FORMS, form, "form")
+    batch, D = gate.shape
+    _rows("gate", gate, gate)
+    _rows("x", x, gate)
+    if state.dim() != 2:
+        raise ValueError("state: expected (slots, D)")
+    _float_state("state", state, (state.shape[0], D), gate)
+    if out_state is None:
+        out_state = state
+    else:
+        _float_state("out_state", out_state, (state.shape[0], D), gate)
+    if slots is not None:
+        if slots.dtype != torch.int32 or slots.shape != (batch,) or (batch > 1 and slots.stride(0) != 1):
+            raise ValueError("slots: a contiguous int32 vector of batch state numbers")
+        if slots.get_device() != gate.get_device():
+            raise ValueError(f"slots: on {slots.device}, expected {gate.device}")
+    y = torch.empty((batch, D), dtype=gate.dtype, device=gate.device)
+    _check("trsm_linrec_step", _on_device(gate, lambda st: _library().trsm_linrec_step(
+        code, kind, batch, D, gate.data_ptr(), gate.stride(0), x.data_ptr(), x.stride(0), _pointer(slots),
+        state.shape[0], state.data_ptr(), state.stride(0), out_state.data_ptr(), out_state.stride(0), y.data_ptr(), D,
+        st)))
+    return y
