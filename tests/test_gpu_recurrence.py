@@ -497,3 +497,22 @@ def test_refusals(env):
     # fewer states than rows: the rows without one are padding
     y = tg.linear_recurrence_step(g[0], g[0], torch.zeros(3, 8, device="cuda"))
     assert torch.all(y[3:] == 0) and torch.equal(y[:3], g[0][:3])
+
+
+def test_expired_wait_is_reported_and_leaves_the_device_usable(env):
+    """A sequence long enough for a cluster, with a wait limit of zero polls:
+    the exchange between the CTAs gives up, the status word says so, and the
+    next call is right again."""
+    torch, tg = env
+    g = torch.rand(1, 5000, 64, device="cuda")
+    x = torch.randn(1, 5000, 64, device="cuda")
+    want, last = tg.linear_recurrence(g, x)
+    assert tg.trsm_device_status() == 0
+    tg.trsm_set_wait_limit(0)
+    try:
+        tg.linear_recurrence(g, x)
+        assert tg.trsm_device_status() == tg.ERR_DEVICE_TIMEOUT
+    finally:
+        tg.trsm_set_wait_limit(-1)
+    h, l2 = tg.linear_recurrence(g, x)
+    assert torch.equal(h, want) and torch.equal(l2, last) and tg.trsm_device_status() == 0

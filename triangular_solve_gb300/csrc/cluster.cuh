@@ -1,5 +1,5 @@
-// Thread-block cluster helpers: rank, barrier, and stores into the shared
-// memory of another CTA of the cluster.
+// Thread-block cluster helpers: rank, barrier, and signalled stores into
+// the shared memory of another CTA of the cluster.
 #pragma once
 
 #include <stdint.h>
@@ -25,8 +25,29 @@ __device__ __forceinline__ uint32_t map(uint32_t addr, uint32_t r) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(o) : "r"(addr), "r"(r));
     return o;
 }
-__device__ __forceinline__ void store_f32x2(uint32_t cluster_addr, float x, float y) {
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};\n" ::"r"(cluster_addr), "f"(x), "f"(y) : "memory");
+// Store into another CTA's shared memory that counts its 8 bytes on that
+// CTA's barrier, which orders it before the waits there.
+__device__ __forceinline__ void send_f32x2(uint32_t cluster_addr, float x, float y, uint32_t cluster_bar) {
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];\n" ::"r"(cluster_addr),
+        "r"(__float_as_uint(x)), "r"(__float_as_uint(y)), "r"(cluster_bar)
+        : "memory");
+}
+// Bounded wait (`limit` polls) for a phase of this CTA's barrier that other
+// CTAs of the cluster complete; false when it expired.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint32_t limit) {
+    for (uint32_t i = 0; i < limit; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (done) return true;
+    }
+    return false;
 }
 __device__ __forceinline__ void sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");

@@ -36,13 +36,13 @@
 
 #include "cluster.cuh"
 #include "common.cuh"
+#include "internal.h"
 #include "linrec.h"
 #include "trsm_model.h"
 
 namespace trsm {
 namespace linrec {
 
-constexpr int kThreads = 256;
 constexpr int kMaxCluster = 8;
 
 template <typename T> __device__ __forceinline__ float to_f32(T v);
@@ -53,6 +53,16 @@ template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Two values rounded to 16 bits, the first in the low half.
+__device__ __forceinline__ void round_pair(float lo, float hi, uint32_t &w, __half) {
+    const __half2 r = __floats2half2_rn(lo, hi);
+    w = *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ void round_pair(float lo, float hi, uint32_t &w, __nv_bfloat16) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+    w = *reinterpret_cast<const uint32_t *>(&r);
+}
 
 // VEC elements of T as one access (VEC * sizeof(T) is 16, or VEC = 1).
 template <typename T, int VEC> struct alignas(VEC * sizeof(T)) Pack {
@@ -66,18 +76,87 @@ template <typename T, int VEC>
 __device__ __forceinline__ void store_pack(T *p, const Pack<T, VEC> &r) {
     *reinterpret_cast<Pack<T, VEC> *>(p) = r;
 }
+// The same from global memory that nothing writes meanwhile, past L1.
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> load_once(const T *p) {
+    if constexpr (VEC * sizeof(T) == 16) {
+        uint4 w;
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                     : "l"(p));
+        return *reinterpret_cast<Pack<T, VEC> *>(&w);
+    } else {
+        return load_pack<T, VEC>(p);
+    }
+}
 
-// 2^x, 2^-22 relative, and 1 / x for x in [1, 2^127), rounded to within a unit
-// in the last place: the hardware's approximation after one Newton step.
+// Arithmetic on the channels of a thread in pairs (one instruction for two
+// single-precision operations), or on one where it has one.
+template <int VEC> struct Lane {
+    using V = f32x2;
+    static constexpr int kCount = VEC / 2;
+};
+template <> struct Lane<1> {
+    using V = float;
+    static constexpr int kCount = 1;
+};
+__device__ __forceinline__ float mul_(float a, float b) { return a * b; }
+__device__ __forceinline__ float add_(float a, float b) { return a + b; }
+__device__ __forceinline__ f32x2 mul_(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 add_(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float mad_(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ f32x2 mad_(f32x2 a, f32x2 b, f32x2 c) { return ffma2(a, b, c); }
+template <typename V> __device__ __forceinline__ V splat(float x);
+template <> __device__ __forceinline__ float splat<float>(float x) { return x; }
+template <> __device__ __forceinline__ f32x2 splat<f32x2>(float x) { return pack2(x, x); }
+// f on each value
+template <typename F> __device__ __forceinline__ float each(float x, F f) { return f(x); }
+template <typename F> __device__ __forceinline__ f32x2 each(f32x2 x, F f) {
+    float lo, hi;
+    unpack2(x, lo, hi);
+    return pack2(f(lo), f(hi));
+}
+
+// Values 2k and 2k + 1 (the one value, VEC = 1) of a pack, and a pack of such.
+template <typename T, int VEC>
+__device__ __forceinline__ typename Lane<VEC>::V value(const Pack<T, VEC> &p, int k) {
+    if constexpr (VEC == 1) return to_f32<T>(p.v[0]);
+    else return pack2(to_f32<T>(p.v[2 * k]), to_f32<T>(p.v[2 * k + 1]));
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void set_value(Pack<T, VEC> &p, int k, typename Lane<VEC>::V x) {
+    if constexpr (VEC == 1) {
+        p.v[0] = from_f32<T>(x);
+    } else {
+        float lo, hi;
+        unpack2(x, lo, hi);
+        if constexpr (sizeof(T) == 4) {
+            p.v[2 * k] = lo;
+            p.v[2 * k + 1] = hi;
+        } else {
+            round_pair(lo, hi, reinterpret_cast<uint32_t *>(&p)[k], T());
+        }
+    }
+}
+
+// The hardware's 2^x (2^-22 relative) and 1 / x (a unit in the last place).
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ float recip_newton(float x) {
+__device__ __forceinline__ float recip_fast(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return fmaf(r, fmaf(-x, r, 1.f), r);
+    return r;
 }
 __device__ __forceinline__ float min_nan(float x, float y) {  // NaN if either is
     float r;
@@ -92,19 +171,24 @@ __device__ __forceinline__ float min_nan(float x, float y) {  // NaN if either i
 //
 // sigmoid: e = exp(-g) held below 2^126, so that neither 1 + e nor e a
 // overflows; a is then 2^-126 where it would be smaller still.
-template <typename T, int FORM>
-__device__ __forceinline__ void open_gate(T gate, float &a, float &rest) {
+template <typename T, int FORM, typename V>
+__device__ __forceinline__ void open_gate(V g, V &a, V &rest) {
     constexpr float kLog2e = 1.44269504f;
-    const float g = to_f32<T>(gate);
     constexpr bool kFull = sizeof(T) == 4;
     if constexpr (FORM == TRSM_GATE_DECAY) {
         a = g;
     } else if constexpr (FORM == TRSM_GATE_LOG) {
-        a = kFull ? expf(g) : exp2_fast(g * kLog2e);
+        if constexpr (kFull) a = each(g, [](float x) { return expf(x); });
+        else a = each(mul_(g, splat<V>(kLog2e)), [](float x) { return exp2_fast(x); });
     } else {
-        const float e = kFull ? min_nan(expf(-g), 0x1p126f) : exp2_fast(min_nan(g * -kLog2e, 126.f));
-        a = recip_newton(1.f + e);
-        rest = e * a;
+        V e;
+        if constexpr (kFull) e = each(g, [](float x) { return min_nan(expf(-x), 0x1p126f); });
+        else e = each(mul_(g, splat<V>(-kLog2e)), [](float x) { return exp2_fast(min_nan(x, 126.f)); });
+        // 1 / (1 + e): the approximation r, then one Newton step
+        const V n = mad_(e, splat<V>(-1.f), splat<V>(-1.f));
+        const V r = each(n, [](float x) { return recip_fast(-x); });
+        a = mad_(r, mad_(n, r, splat<V>(1.f)), r);
+        rest = mul_(e, a);
     }
 }
 
@@ -138,33 +222,45 @@ __device__ __forceinline__ Walk<T> walk(const LinrecRows &r, const Sequence &s, 
     return {first, r.st};
 }
 
-// Shapes and shared memory of one instantiation.
-template <typename T, int FORM, bool BWD, int VEC, int LANES, int ROWS> struct Shape {
-    static constexpr int kChannels = LANES * VEC;               // channels of a CTA
-    static constexpr int kStretch = kThreads / LANES * ROWS;    // tokens of a CTA in one step
-    static __device__ __forceinline__ int channel_at(int i) {   // see slot_A
+// One way to run the scan: THREADS threads, ROWS tokens a thread, STAGES
+// buffers of the gate and x (backward: dh); SIDE: the backward pass's h and x
+// are staged too, else they wait in registers.  BLOCKS: CTAs an SM should hold.
+template <int VEC_, int LANES_, int THREADS, int ROWS_, int STAGES_, bool SIDE_, int BLOCKS> struct Plan {
+    static constexpr int VEC = VEC_, LANES = LANES_, kThreads = THREADS, ROWS = ROWS_, STAGES = STAGES_, kBlocks = BLOCKS;
+    static constexpr bool SIDE = SIDE_;
+    static constexpr int kChannels = LANES * VEC;      // channels of a CTA
+    static constexpr int kSlots = THREADS / LANES;     // time slots of a CTA
+    static constexpr int kStretch = kSlots * ROWS;     // tokens of a CTA in one step
+    static constexpr int kParts = THREADS / kChannels, kPartSlots = kSlots / kParts;
+    static constexpr int kBufferElems = kStretch * kChannels;
+    static_assert(THREADS % kChannels == 0 && kSlots % kParts == 0, "threads per channel");
+    // see slot_A
+    static __device__ __forceinline__ int channel_at(int i) {
         constexpr int q = VEC < 4 ? VEC : 4;
         return (i / q) % LANES * VEC + i / (q * LANES) * q + i % q;
     }
-    static constexpr bool kSigmoid = FORM == TRSM_GATE_SIGMOID;
-    // two buffers each of the gate and x (backward: dh), and in the backward
-    // pass one each of h and (sigmoid) x
-    static constexpr int kBuffers = 4 + (BWD ? 1 + (kSigmoid ? 1 : 0) : 0);
-    static constexpr int kBufferElems = kStretch * kChannels;
-    static constexpr size_t kSmem = (size_t)kBuffers * kBufferElems * sizeof(T);
+    template <typename T, int FORM, bool BWD> static constexpr int buffers() {
+        return 2 * STAGES + (BWD && SIDE ? (FORM == TRSM_GATE_SIGMOID ? 2 : 1) : 0);
+    }
+    template <typename T, int FORM, bool BWD> static constexpr size_t smem() {
+        return (size_t)buffers<T, FORM, BWD>() * kBufferElems * sizeof(T);
+    }
 };
 
-template <typename T, int FORM, bool BWD, int VEC, int LANES, int ROWS>
-__global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant__ LinrecArgs g, const int groups) {
-    using S = Shape<T, FORM, BWD, VEC, LANES, ROWS>;
-    constexpr int kChannels = S::kChannels, kStretch = S::kStretch;
-    constexpr int kSlots = kThreads / LANES, kParts = kThreads / kChannels, kPartSlots = kSlots / kParts;
-    constexpr bool kSigmoid = S::kSigmoid;
+template <typename T, int FORM, bool BWD, typename L>
+__global__ void __launch_bounds__(L::kThreads, L::kBlocks)
+    scan_kernel(const __grid_constant__ LinrecArgs g, const int groups) {
+    constexpr int VEC = L::VEC, LANES = L::LANES, ROWS = L::ROWS;
+    constexpr int kChannels = L::kChannels, kStretch = L::kStretch;
+    constexpr int kSlots = L::kSlots, kParts = L::kParts, kPartSlots = L::kPartSlots;
+    constexpr bool kSigmoid = FORM == TRSM_GATE_SIGMOID;
     // The forward sigmoid keeps a and u of its tokens between the two walks
-    // (their exponential and reciprocal cost more than the registers); the
-    // others open the gate again.
-    constexpr bool kKeep = kSigmoid && !BWD;
+    // where they are few (their exponential and reciprocal cost more than the
+    // registers); otherwise the gate is opened again.
+    constexpr bool kKeep = kSigmoid && !BWD && ROWS * VEC <= 32;
     using P = Pack<T, VEC>;
+    using V = typename Lane<VEC>::V;
+    constexpr int kN = Lane<VEC>::kCount;
 
     extern __shared__ __align__(16) unsigned char staged[];
     // Channels in shared memory stand in the order of the threads' 16-byte
@@ -186,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
     const int len = live ? seq.len : 0;  // tokens this thread may touch
 
     // each of them carries the state of its channel from step to step
-    const int64_t dc = c0 + S::channel_at(place);
+    const int64_t dc = c0 + L::channel_at(place);
     float carry = 0.f;
     if (dc < g.D) {
         if constexpr (BWD) {
@@ -195,11 +291,25 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
             if (g.h0) carry = g.h0[b * g.h0_stride + dc];
         }
     }
-    if (csize > 1) cluster::sync();  // every CTA has started before any writes into its shared memory
+    // Each CTA's pairs arrive in every CTA's cta_pair by stores that count
+    // their bytes on that CTA's barrier; two buffers and barriers by turns.  A
+    // buffer is written again two steps on, by a CTA that then has this one's
+    // pairs of the step between, sent after it had read the buffer.
+    __shared__ __align__(8) uint64_t exchange[2];
+    __shared__ int expired;
+    if (csize > 1) {
+        if (tid == 0) {
+            mbar_init(smem_u32(&exchange[0]), 1);
+            mbar_init(smem_u32(&exchange[1]), 1);
+            expired = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+        }
+        cluster::sync();  // every CTA's barriers exist before any signals them
+    }
 
     // this thread's place in staged buffer i, row r: mine(i)[r * kChannels]
     auto mine = [&](int i) {
-        return reinterpret_cast<T *>(staged) + i * S::kBufferElems + slot * ROWS * kChannels + col * VEC;
+        return reinterpret_cast<T *>(staged) + i * L::kBufferElems + slot * ROWS * kChannels + col * VEC;
     };
     // Copies positions base .. base + ROWS - 1 (those below `end`) into buffer i.
     auto stage = [&](const Walk<const T> &w, int base, int end, int i) {
@@ -226,47 +336,70 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
     const int step = csize * kStretch;
     const int steps = (seq.len + step - 1) / step;
     int base = crank * kStretch + slot * ROWS;  // this thread's first position
-    stage(wg, base, len, 0);
-    stage(wu, base, len, 1);
-    cp_async_commit();
-    int parity = 0;
-    for (int i = 0; i < steps; ++i, base += step, parity ^= 1) {
-        const T *pg = mine(2 * parity), *pu = mine(2 * parity + 1);
-        if constexpr (BWD) {
-            // for the second walk: the row before each token (the last
-            // position is row 0, whose state before is h0), and x
+    // the next step's gate and x (dh) into buffer pair `i`
+    auto stage_next = [&](int at, int i) {
+        stage(wg, at, len, 2 * i);
+        stage(wu, at, len, 2 * i + 1);
+    };
+    // for the backward pass's second walk: the row before each token (the last
+    // position is row 0, whose state before is h0), and x
+    auto stage_side = [&](int at) {
+        if constexpr (BWD && L::SIDE) {
             const Walk<const T> wh = walk<const T, BWD>(g.h, seq, d);
-            stage({wh.at + wh.step, wh.step}, base, len - 1, 4);
-            if constexpr (kSigmoid) stage(walk<const T, BWD>(g.x, seq, d), base, len, 5);
-            cp_async_commit();
+            stage({wh.at + wh.step, wh.step}, at, len - 1, 2 * L::STAGES);
+            if constexpr (kSigmoid) stage(walk<const T, BWD>(g.x, seq, d), at, len, 2 * L::STAGES + 1);
         }
-        stage(wg, base + step, len, 2 * (parity ^ 1));
-        stage(wu, base + step, len, 2 * (parity ^ 1) + 1);
-        cp_async_commit();
-        cp_async_wait<BWD ? 2 : 1>();  // this step's gate and x (dh)
+    };
+    stage_next(base, 0);
+    stage_side(base);
+    cp_async_commit();
+    int parity = 0, i = 0;
+    for (; i < steps; ++i, base += step, parity ^= 1) {
+        const T *pg = mine(L::STAGES == 2 ? 2 * parity : 0), *pu = mine(L::STAGES == 2 ? 2 * parity + 1 : 1);
+        P rh[BWD && !L::SIDE ? ROWS : 1], rx[BWD && !L::SIDE && kSigmoid ? ROWS : 1];
+        if constexpr (BWD && !L::SIDE) {
+            const Walk<const T> wh = walk<const T, BWD>(g.h, seq, d);
+            const T *ph = wh.at + (base + 1) * wh.step;
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+                if (base + r + 1 < len) rh[r] = load_once<T, VEC>(ph + r * wh.step);
+            if constexpr (kSigmoid) {
+                const Walk<const T> wx = walk<const T, BWD>(g.x, seq, d);
+                const T *px = wx.at + base * wx.step;
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r)
+                    if (base + r < len) rx[r] = load_once<T, VEC>(px + r * wx.step);
+            }
+        }
+        if constexpr (L::STAGES == 2) {
+            stage_next(base + step, parity ^ 1);
+            cp_async_commit();
+            cp_async_wait<1>();
+        } else {
+            cp_async_wait<0>();
+        }
 
         // first walk: (A, H) of the slot
-        float a[kKeep ? ROWS : 1][VEC], u[kKeep ? ROWS : 1][VEC];
-        alignas(16) float A[VEC], H[VEC];
+        V a[kKeep ? ROWS : 1][kN], u[kKeep ? ROWS : 1][kN], A[kN], H[kN];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            A[v] = 1.f;
-            H[v] = 0.f;
+        for (int k = 0; k < kN; ++k) {
+            A[k] = splat<V>(1.f);
+            H[k] = splat<V>(0.f);
         }
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
             if (base + r < len) {
                 const P q = load_pack<T, VEC>(pg + r * kChannels), e = load_pack<T, VEC>(pu + r * kChannels);
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    float at, ut = to_f32<T>(e.v[v]), rest;
-                    open_gate<T, FORM>(q.v[v], at, rest);
-                    if constexpr (kSigmoid && !BWD) ut *= rest;
-                    H[v] = BWD ? at * (H[v] + ut) : fmaf(at, H[v], ut);
-                    A[v] *= at;
+                for (int k = 0; k < kN; ++k) {
+                    V at, rest, ut = value(e, k);
+                    open_gate<T, FORM>(value(q, k), at, rest);
+                    if constexpr (kSigmoid && !BWD) ut = mul_(ut, rest);
+                    H[k] = BWD ? mul_(at, add_(H[k], ut)) : mad_(at, H[k], ut);
+                    A[k] = mul_(A[k], at);
                     if constexpr (kKeep) {
-                        a[r][v] = at;
-                        u[r][v] = ut;
+                        a[r][k] = at;
+                        u[r][k] = ut;
                     }
                 }
             }
@@ -278,8 +411,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
 #pragma unroll
         for (int v = 0; v < VEC; v += kQuad) {
             const int at = v * LANES + col * kQuad;
-            store_pack<float, kQuad>(&slot_A[slot][at], *reinterpret_cast<const Pack<float, kQuad> *>(&A[v]));
-            store_pack<float, kQuad>(&slot_H[slot][at], *reinterpret_cast<const Pack<float, kQuad> *>(&H[v]));
+            Pack<float, kQuad> qa, qh;
+#pragma unroll
+            for (int k = 0; k < (kQuad + 1) / 2; ++k) {
+                set_value(qa, k, A[(v + 1) / 2 + k]);
+                set_value(qh, k, H[(v + 1) / 2 + k]);
+            }
+            store_pack<float, kQuad>(&slot_A[slot][at], qa);
+            store_pack<float, kQuad>(&slot_H[slot][at], qh);
         }
         __syncthreads();
         float sa[kPartSlots], sh[kPartSlots];
@@ -295,50 +434,56 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
             part_pair[part][place] = make_float2(pa, ph);
         }
         __syncthreads();
-        if (csize > 1) {
-            if (part == 0) {
-                float ca = 1.f, ch = 0.f;
+        float2 parts[kParts];
 #pragma unroll
-                for (int k = 0; k < kParts; ++k) {
-                    const float2 q = part_pair[k][place];
-                    ch = apply(q.x, q.y, ch);
-                    ca *= q.x;
-                }
-                const uint32_t at = smem_u32(&cta_pair[parity][crank][place]);
-                for (int k = 0; k < csize; ++k) cluster::store_f32x2(cluster::map(at, k), ca, ch);
-            }
-            // Two buffers by turns: a CTA writes a buffer again only after the
-            // next step's barrier, which all pass after reading it.
-            cluster::sync();
-        }
+        for (int k = 0; k < kParts; ++k) parts[k] = part_pair[k][place];
         float state = carry;
         if (csize > 1) {
-            for (int k = 0; k < csize; ++k) {
+            float ca = 1.f, ch = 0.f;
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) {
+                ch = apply(parts[k].x, parts[k].y, ch);
+                ca *= parts[k].x;
+            }
+            const uint32_t at = smem_u32(&cta_pair[parity][crank][place]), bar = smem_u32(&exchange[parity]);
+            if (tid == 0) mbar_expect_tx(bar, (uint32_t)(csize * kChannels * sizeof(float2)));
+            for (int k = part; k < csize; k += kParts)
+                cluster::send_f32x2(cluster::map(at, k), ca, ch, cluster::map(bar, k));
+            if (!cluster::wait(bar, (i >> 1) & 1, g.wait_limit)) {
+                record_timeout(g.status);
+                *(volatile int *)&expired = 1;
+            }
+            float2 ctas[kMaxCluster];
+#pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k)
+                if (k < csize) ctas[k] = cta_pair[parity][k][place];
+#pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k) {
                 if (k == crank) state = carry;
-                const float2 q = cta_pair[parity][k][place];
-                carry = apply(q.x, q.y, carry);
+                if (k < csize) carry = apply(ctas[k].x, ctas[k].y, carry);
             }
         }
 #pragma unroll
         for (int k = 0; k < kParts; ++k) {
-            const float2 q = part_pair[k][place];
-            if (k < part) state = apply(q.x, q.y, state);
-            if (csize == 1) carry = apply(q.x, q.y, carry);
+            if (k < part) state = apply(parts[k].x, parts[k].y, state);
+            if (csize == 1) carry = apply(parts[k].x, parts[k].y, carry);
         }
 #pragma unroll
         for (int k = 0; k < kPartSlots; ++k) {
             slot_H[part * kPartSlots + k][place] = state;
             state = apply(sa[k], sh[k], state);
         }
-        if constexpr (BWD) cp_async_wait<1>();  // h and x
         __syncthreads();
+        if (csize > 1 && *(volatile int *)&expired) break;  // seen by all threads alike
 
         // second walk, from the slot's starting state
-        alignas(16) float h[VEC];
+        V h[kN];
 #pragma unroll
-        for (int v = 0; v < VEC; v += kQuad)
-            *reinterpret_cast<Pack<float, kQuad> *>(&h[v]) =
-                load_pack<float, kQuad>(&slot_H[slot][v * LANES + col * kQuad]);
+        for (int v = 0; v < VEC; v += kQuad) {
+            const Pack<float, kQuad> q = load_pack<float, kQuad>(&slot_H[slot][v * LANES + col * kQuad]);
+#pragma unroll
+            for (int k = 0; k < (kQuad + 1) / 2; ++k) h[(v + 1) / 2 + k] = value(q, k);
+        }
         if constexpr (!BWD) {
             const Walk<T> wo = walk<T, BWD>(g.h, seq, d);
             T *out = wo.at + base * wo.step;
@@ -351,17 +496,17 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
                         e = load_pack<T, VEC>(pu + r * kChannels);
                     }
 #pragma unroll
-                    for (int v = 0; v < VEC; ++v) {
-                        float at, ut, rest;
+                    for (int k = 0; k < kN; ++k) {
+                        V at, ut, rest;
                         if constexpr (kKeep) {
-                            at = a[r][v];
-                            ut = u[r][v];
+                            at = a[r][k];
+                            ut = u[r][k];
                         } else {
-                            open_gate<T, FORM>(q.v[v], at, rest);
-                            ut = to_f32<T>(e.v[v]);
+                            open_gate<T, FORM>(value(q, k), at, rest);
+                            ut = value(e, k);
                         }
-                        h[v] = fmaf(at, h[v], ut);
-                        o.v[v] = from_f32<T>(h[v]);
+                        h[k] = mad_(at, h[k], ut);
+                        set_value(o, k, h[k]);
                     }
                     store_pack<T, VEC>(out + r * wo.step, o);
                 }
@@ -369,38 +514,63 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(const __grid_constant
         } else {
             const Walk<T> wo = walk<T, BWD>(g.dgate, seq, d), wx = walk<T, BWD>(g.dx, seq, d);
             T *og = wo.at + base * wo.step, *ox = wx.at + base * wx.step;
-            const T *ph = mine(4), *px = mine(S::kBuffers - 1);
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
                 if (base + r < len) {
                     const P q = load_pack<T, VEC>(pg + r * kChannels), e = load_pack<T, VEC>(pu + r * kChannels);
-                    P before, in, o0, o1;
-                    const bool start = base + r + 1 == len;
-                    if (!start) before = load_pack<T, VEC>(ph + r * kChannels);
-                    if constexpr (kSigmoid) in = load_pack<T, VEC>(px + r * kChannels);
+                    P o0, o1, before, in;
+                    if constexpr (L::SIDE) {
+                        before = load_pack<T, VEC>(mine(2 * L::STAGES) + r * kChannels);
+                        if constexpr (kSigmoid) in = load_pack<T, VEC>(mine(2 * L::STAGES + 1) + r * kChannels);
+                    } else {
+                        before = rh[r];
+                        if constexpr (kSigmoid) in = rx[r];
+                    }
+                    const bool start = base + r + 1 == len;  // row 0: the state before it is h0
+                    Pack<float, VEC> first = {};
+                    if (start && g.h0) {
 #pragma unroll
-                    for (int v = 0; v < VEC; ++v) {
-                        float at, rest;
-                        open_gate<T, FORM>(q.v[v], at, rest);
-                        const float prev = !start ? to_f32<T>(before.v[v])
-                                                  : g.h0 ? g.h0[b * g.h0_stride + d + v] : 0.f;
-                        const float full = to_f32<T>(e.v[v]) + h[v];
-                        h[v] = at * full;
+                        for (int v = 0; v < VEC; ++v) first.v[v] = g.h0[b * g.h0_stride + d + v];
+                    }
+#pragma unroll
+                    for (int k = 0; k < kN; ++k) {
+                        V at, rest;
+                        open_gate<T, FORM>(value(q, k), at, rest);
+                        const V prev = start ? value(first, k) : value(before, k);
+                        const V full = add_(value(e, k), h[k]);
+                        h[k] = mul_(at, full);
                         if constexpr (FORM == TRSM_GATE_DECAY) {
-                            o0.v[v] = from_f32<T>(full * prev);
-                            o1.v[v] = from_f32<T>(full);
+                            set_value(o0, k, mul_(full, prev));
+                            set_value(o1, k, full);
                         } else if constexpr (FORM == TRSM_GATE_LOG) {
-                            o0.v[v] = from_f32<T>(h[v] * prev);
-                            o1.v[v] = from_f32<T>(full);
+                            set_value(o0, k, mul_(h[k], prev));
+                            set_value(o1, k, full);
                         } else {
-                            o0.v[v] = from_f32<T>((prev - to_f32<T>(in.v[v])) * (h[v] * rest));
-                            o1.v[v] = from_f32<T>(full * rest);
+                            const V gap = mad_(value(in, k), splat<V>(-1.f), prev);
+                            set_value(o0, k, mul_(gap, mul_(h[k], rest)));
+                            set_value(o1, k, mul_(full, rest));
                         }
                     }
                     store_pack<T, VEC>(og + r * wo.step, o0);
                     store_pack<T, VEC>(ox + r * wx.step, o1);
                 }
             }
+        }
+        if constexpr (L::STAGES == 1) {  // this thread has read its own places
+            stage_next(base + step, 0);
+            if constexpr (L::SIDE) stage_side(base + step);
+            cp_async_commit();
+        } else if constexpr (L::SIDE) {
+            stage_side(base + step);
+            cp_async_commit();
+        }
+    }
+    cp_async_wait_all();
+    if (csize > 1) {
+        cluster::sync();  // no CTA leaves while another may still send to it
+        if (*(volatile int *)&expired) {  // ... nor before what was sent has landed
+            if (tid == 0) cluster::wait(smem_u32(&exchange[parity]), (i >> 1) & 1, kWaitLimit);
+            __syncthreads();
         }
     }
     if (g.last && crank == 0 && part == 0 && dc < g.D) g.last[b * g.D + dc] = carry;
@@ -428,12 +598,13 @@ __global__ void __launch_bounds__(128) step_kernel(const __grid_constant__ Linre
         // plain accesses: next may be state
         S h = *reinterpret_cast<const S *>(g.state + s * g.state_stride + d);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            float a, rest, u = to_f32<T>(px.v[v]);
-            open_gate<T, FORM>(pg.v[v], a, rest);
-            if constexpr (FORM == TRSM_GATE_SIGMOID) u *= rest;
-            h.v[v] = fmaf(a, h.v[v], u);
-            o.v[v] = from_f32<T>(h.v[v]);
+        for (int k = 0; k < Lane<VEC>::kCount; ++k) {
+            typename Lane<VEC>::V a, rest, u = value(px, k);
+            open_gate<T, FORM>(value(pg, k), a, rest);
+            if constexpr (FORM == TRSM_GATE_SIGMOID) u = mul_(u, rest);
+            const auto next = mad_(a, value(h, k), u);
+            set_value(h, k, next);
+            set_value(o, k, next);
         }
         *reinterpret_cast<S *>(g.next + s * g.next_stride + d) = h;
         store_pack<T, VEC>(y, o);
@@ -462,27 +633,29 @@ inline bool rows_vec(const LinrecArgs &a, const LinrecRows &r, int64_t elem) {
     return bits % 16 == 0;
 }
 
-template <typename T, int FORM, bool BWD, int VEC, int LANES, int ROWS>
-int launch_scan(const LinrecArgs &a, cudaStream_t st) {
-    using S = Shape<T, FORM, BWD, VEC, LANES, ROWS>;
+template <typename T, int FORM, bool BWD, typename L>
+int launch_scan(LinrecArgs a, cudaStream_t st) {
+    constexpr size_t kSmem = L::template smem<T, FORM, BWD>();
     int sms = 0;
-    const int rc = sm_count(&sms);
+    int rc = sm_count(&sms);
+    if (!rc) rc = device_status_word(&a.status);
+    a.wait_limit = first_wait_limit();
     if (rc) return rc;
-    const int64_t groups = (a.D + LANES * VEC - 1) / (LANES * VEC);
+    const int64_t groups = (a.D + L::kChannels - 1) / L::kChannels;
     const int64_t units = a.batch * groups;
     // CTAs along a sequence: until the GPU is full, but no more than it has stretches
     const int64_t len = a.offsets ? (a.T + a.batch - 1) / a.batch : a.T;
     int cs = 1;
-    while (cs < kMaxCluster && units * cs < 4 * sms && cs * S::kStretch < len) cs *= 2;
+    while (cs < kMaxCluster && units * cs < 4 * sms && cs * L::kStretch < len) cs *= 2;
     if (units * cs > 0x7fffffff) return -3;
-    auto *kernel = scan_kernel<T, FORM, BWD, VEC, LANES, ROWS>;
+    auto *kernel = scan_kernel<T, FORM, BWD, L>;
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return cuda_status(e);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * cs));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.blockDim = dim3(L::kThreads);
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -499,8 +672,8 @@ int run(const LinrecArgs &a, cudaStream_t st) {
     bool vec = a.D % kVec == 0 && rows_vec(a, a.gate, sizeof(T)) && rows_vec(a, a.h, sizeof(T));
     if (!BWD || FORM == TRSM_GATE_SIGMOID) vec = vec && rows_vec(a, a.x, sizeof(T));
     if (BWD) vec = vec && rows_vec(a, a.dh, sizeof(T)) && rows_vec(a, a.dgate, sizeof(T)) && rows_vec(a, a.dx, sizeof(T));
-    if (vec) return launch_scan<T, FORM, BWD, kVec, 8, 32 / kVec>(a, st);
-    return launch_scan<T, FORM, BWD, 1, 32, 8>(a, st);
+    if (vec) return launch_scan<T, FORM, BWD, Plan<kVec, 8, 256, 32 / kVec, 2, false, 2>>(a, st);
+    return launch_scan<T, FORM, BWD, Plan<1, 32, 256, 8, 2, false, 2>>(a, st);
 }
 
 template <typename T>

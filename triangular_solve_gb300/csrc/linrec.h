@@ -24,6 +24,8 @@ struct LinrecArgs {
     const float *dh_last;   // backward, may be null
     float *last;            // forward: h_last, backward: dh0; may be null
     const int32_t *offsets; // packed sequences, may be null
+    int *status;            // device status word of the bounded waits
+    uint32_t wait_limit;    // their polls
 };
 
 struct LinrecStepArgs {
