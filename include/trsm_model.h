@@ -124,6 +124,48 @@ int trsm_linrec_step(trsm_elem_t dtype, trsm_gate_t form, int64_t batch, int64_t
                      const float *state, int64_t state_stride, float *next, int64_t next_stride, void *y,
                      int64_t y_stride, void *stream);
 
+/*
+ * Orthogonalisation by Newton-Schulz products: for each of `batch` row-major
+ * m x n matrices G (row stride ldg >= n, matrix b at G + b*strideG),
+ *
+ *     X_0 = G / (|G|_F + eps),
+ *     X_{k+1} = (a_k I + b_k S + c_k S^2) X_k,   S = X_k X_k^T,
+ *
+ * k = 0 .. steps - 1 (on the transposed matrix where m > n, so that S has the
+ * smaller order), and O = X_steps (row stride ldo, matrices strideO apart).
+ * Each step maps every singular value s to a_k s + b_k s^3 + c_k s^5.
+ * coef: HOST array of 3 * steps doubles (a_0, b_0, c_0, a_1, ...), read before
+ * the call returns; NULL: 3.4445, -4.7750, 2.0315 in every step, which takes
+ * singular values above 0.003 to between 0.7 and 1.2 in five steps.  A column-major
+ * matrix is the row-major one of its transpose, and the result likewise.
+ *
+ * in_dtype: F32, F16 or BF16; out_dtype: F16 or BF16.  The products run on the
+ * tensor cores with f16 factors (11 bits) and f32 sums; X_k is held as an f16
+ * head and tail where the steps to come would amplify its rounding more than
+ * 16 times, so the result is near its own 16-bit rounding (about 3e-3
+ * relative to |O|_F) also for matrices close to low rank.  steps = 0 gives
+ * X_0.  A matrix with a NaN or infinity gives NaN throughout, and no other
+ * matrix of the batch is affected.  G and O must not overlap, nor the
+ * matrices of O each other.
+ *
+ * workspace: device pointer, 256-byte aligned, of ws_bytes >=
+ * trsm_orthogonalize_workspace_bytes(in_dtype, m, n, batch, steps) bytes, in
+ * use until the call's work on `stream` is done; or NULL (ws_bytes ignored) to
+ * take it, ordered on `stream`, from the library's pool (see trsm_llnn).
+ *
+ * m and n are at most 65536, batch at most 65535 and steps at most 64.
+ *
+ * Arguments: 1 in_dtype, 2 out_dtype, 3 m, 4 n, 5 G, 6 ldg, 7 strideG, 8 O,
+ * 9 ldo, 10 strideO, 11 batch, 12 steps, 13 coef, 14 eps, 15 workspace,
+ * 16 ws_bytes, 17 stream.
+ */
+int trsm_orthogonalize(trsm_elem_t in_dtype, trsm_elem_t out_dtype, int64_t m, int64_t n, const void *G, int64_t ldg,
+                       int64_t strideG, void *O, int64_t ldo, int64_t strideO, int64_t batch, int64_t steps,
+                       const double *coef, double eps, void *workspace, size_t ws_bytes, void *stream);
+
+/* Workspace of trsm_orthogonalize in bytes; (size_t)-1 for invalid arguments. */
+size_t trsm_orthogonalize_workspace_bytes(trsm_elem_t in_dtype, int64_t m, int64_t n, int64_t batch, int64_t steps);
+
 #ifdef __cplusplus
 }
 #endif

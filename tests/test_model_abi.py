@@ -94,3 +94,42 @@ def test_cpu_tensors_are_refused():
         tg.linear_recurrence_step(g[0], g[0], g[0])
     with pytest.raises(ValueError, match="CPU tensor"):
         tg.linear_recurrence(g.requires_grad_(), g)
+
+
+ORTH = [2, 2, 4, 6, FAKE, 6, 24, FAKE, 6, 24, 2, 5, None, 1e-7, FAKE, 1 << 30, None]
+
+
+@pytest.mark.parametrize("pos,bad", [
+    (1, 3), (2, 0), (2, 3), (3, -1), (3, 65537), (4, -1), (4, 65537), (5, None), (5, FAKE + 1), (6, 5), (7, -1),
+    (8, None), (8, FAKE + 1), (9, 5), (10, 23), (11, -1), (11, 65536), (12, -1), (12, 65), (14, -1.0),
+    (14, float("nan"))])
+def test_orthogonalize_argument_errors_report_position(lib, pos, bad):
+    args = list(ORTH)
+    args[pos - 1] = bad
+    assert lib.trsm_orthogonalize(*args) == -pos
+
+
+def test_orthogonalize_workspace(lib):
+    args = list(ORTH)
+    args[15] = tg.trsm_orthogonalize_workspace_bytes("bf16", 4, 6, 2) - 1
+    assert lib.trsm_orthogonalize(*args) == tg.ERR_WORKSPACE
+    args[14], args[15] = FAKE + 8, 1 << 30
+    assert lib.trsm_orthogonalize(*args) == tg.ERR_WORKSPACE
+    assert tg.trsm_orthogonalize_workspace_bytes("f32", 0, 6, 2) == 0
+    assert tg.trsm_orthogonalize_workspace_bytes("f32", 6, 4, 2) == tg.trsm_orthogonalize_workspace_bytes("f32", 4, 6, 2)
+    for bad in (dict(m=-1), dict(n=65537), dict(batch=-1), dict(steps=65)):
+        with pytest.raises(ValueError):
+            tg.trsm_orthogonalize_workspace_bytes(**(dict(in_dtype="f32", m=4, n=6, batch=1) | bad))
+    for pos in (3, 4, 11):  # nothing to do
+        args = list(ORTH)
+        args[pos - 1], args[4], args[7] = 0, None, None
+        assert lib.trsm_orthogonalize(*args) == 0
+
+
+def test_coefficients():
+    assert list(model._coefficients(2, (1, 2, 3))) == [1, 2, 3, 1, 2, 3]
+    assert list(model._coefficients(2, [(1, 2, 3), (4, 5, 6)])) == [1, 2, 3, 4, 5, 6]
+    assert model._coefficients(5, None) is None and list(model._coefficients(0, None) or []) == []
+    for bad in ((1, 2), [(1, 2, 3), (4, 5)]):
+        with pytest.raises(ValueError):
+            model._coefficients(2, bad)

@@ -26,6 +26,7 @@ __all__ = [
     "library_path", "load_library",
     "trsm_linrec_forward", "trsm_linrec_backward", "trsm_linrec_step",
     "linear_recurrence", "linear_recurrence_backward", "linear_recurrence_step",
+    "trsm_orthogonalize", "trsm_orthogonalize_workspace_bytes", "orthogonalize",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -334,5 +335,5 @@ def solve(A, B, alpha=1.0, stream=None):
 
 # the operators of include/trsm_model.h
 from .model import (  # noqa: E402
-    linear_recurrence, linear_recurrence_backward, linear_recurrence_step, trsm_linrec_backward,
-    trsm_linrec_forward, trsm_linrec_step)
+    linear_recurrence, linear_recurrence_backward, linear_recurrence_step, orthogonalize, trsm_linrec_backward,
+    trsm_linrec_forward, trsm_linrec_step, trsm_orthogonalize, trsm_orthogonalize_workspace_bytes)

@@ -4,7 +4,9 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "internal.h"
 #include "linrec.h"
+#include "orth.h"
 #include "trsm_model.h"
 
 using namespace trsm;
@@ -28,6 +30,9 @@ bool known_form(int form) { return form == TRSM_GATE_DECAY || form == TRSM_GATE_
 constexpr int64_t kMaxT = 0x7fff0000;  // positions are counted in int
 
 // Output rows: each D long, disjoint (packed: one list of rows).
+constexpr double kDefaultCoef[3] = {3.4445, -4.7750, 2.0315};
+constexpr int64_t kMaxSteps = 64;
+
 int64_t magnitude(int64_t v) { return v < 0 ? -v : v; }
 bool rows_disjoint(int64_t rows, int64_t D, int64_t st) { return rows <= 1 || magnitude(st) >= D; }
 
@@ -154,6 +159,56 @@ int trsm_linrec_step(trsm_elem_t dtype, trsm_gate_t form, int64_t batch, int64_t
         case TRSM_ELEM_F16: return linrec_step_f16(a, (int)form, st);
         default: return linrec_step_bf16(a, (int)form, st);
     }
+}
+
+int trsm_orthogonalize(trsm_elem_t in_dtype, trsm_elem_t out_dtype, int64_t m, int64_t n, const void *G, int64_t ldg,
+                       int64_t strideG, void *O, int64_t ldo, int64_t strideO, int64_t batch, int64_t steps,
+                       const double *coef, double eps, void *workspace, size_t ws_bytes, void *stream) {
+    const int64_t es = elem_size((int)in_dtype);
+    if (!es) return -1;
+    if (out_dtype != TRSM_ELEM_F16 && out_dtype != TRSM_ELEM_BF16) return -2;
+    if (m < 0 || m > 65536) return -3;
+    if (n < 0 || n > 65536) return -4;
+    if (batch < 0 || batch > 65535) return -11;
+    if (steps < 0 || steps > kMaxSteps) return -12;
+    if (!(eps >= 0)) return -14;
+    if (m == 0 || n == 0 || batch == 0) return TRSM_SUCCESS;
+    if (!good(G, es)) return -5;
+    if (m > 1 && ldg < n) return -6;
+    if (batch > 1 && strideG < 0) return -7;
+    if (!good(O, 2)) return -8;
+    if (m > 1 && ldo < n) return -9;
+    if (batch > 1 && strideO < (m - 1) * ldo + n) return -10;
+    const size_t need = orth_workspace_bytes((int)in_dtype, m, n, batch, steps);
+    if (workspace && (!good(workspace, 256) || ws_bytes < need)) return TRSM_ERR_WORKSPACE;
+    double defaults[3 * kMaxSteps];
+    if (!coef) {
+        for (int64_t k = 0; k < steps; ++k)
+            for (int i = 0; i < 3; ++i) defaults[3 * k + i] = kDefaultCoef[i];
+        coef = defaults;
+    }
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    void *ws = workspace;
+    if (!ws) {
+        const int rc = workspace_alloc(&ws, need, st);
+        if (rc) return rc;
+    }
+    const OrthArgs a = {(int)in_dtype, (int)out_dtype, m, n, G, ldg, strideG, O, ldo, strideO, batch, (int)steps, coef,
+                        eps, ws};
+    int rc = orth_run(a, st);
+    if (!workspace) {
+        const cudaError_t e = cudaFreeAsync(ws, st);
+        if (!rc && e != cudaSuccess) rc = cuda_status(e);
+    }
+    return rc;
+}
+
+size_t trsm_orthogonalize_workspace_bytes(trsm_elem_t in_dtype, int64_t m, int64_t n, int64_t batch, int64_t steps) {
+    if (!elem_size((int)in_dtype) || m < 0 || m > 65536 || n < 0 || n > 65536 || batch < 0 || batch > 65535 ||
+        steps < 0 || steps > kMaxSteps)
+        return (size_t)-1;
+    if (m == 0 || n == 0 || batch == 0) return 0;
+    return orth_workspace_bytes((int)in_dtype, m, n, batch, steps);
 }
 
 }  // extern "C"

@@ -1,0 +1,26 @@
+// Internal interface of the Newton-Schulz orthogonalisation (orth.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace trsm {
+
+struct OrthArgs {
+    int in_dtype, out_dtype;
+    int64_t m, n;
+    const void *G;
+    int64_t ldg, strideG;
+    void *O;
+    int64_t ldo, strideO;
+    int64_t batch;
+    int steps;
+    const double *coef;  // 3 a step
+    double eps;
+    void *ws;
+};
+size_t orth_workspace_bytes(int in_dtype, int64_t m, int64_t n, int64_t batch, int64_t steps);
+int orth_run(const OrthArgs &a, cudaStream_t st);
+
+}  // namespace trsm

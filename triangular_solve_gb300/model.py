@@ -1,11 +1,13 @@
 """Python binding of the operators of ``include/trsm_model.h``: the gated
 linear recurrence (forward, backward, single tokens) of recurrent sequence
-models, next to the triangular solves it is a special case of.
+models, next to the triangular solves it is a special case of, and the
+orthogonalisation of an update matrix by Newton-Schulz products.
 
-``trsm_linrec_*`` mirror the C ABI one to one.  ``linear_recurrence`` (which
-is differentiable), ``linear_recurrence_backward`` and
-``linear_recurrence_step`` take torch tensors, check them, allocate the
-outputs and run on the tensors' device and torch's current stream.
+``trsm_linrec_*`` and ``trsm_orthogonalize*`` mirror the C ABI one to one.
+``linear_recurrence`` (which is differentiable), ``linear_recurrence_backward``,
+``linear_recurrence_step`` and ``orthogonalize`` take torch tensors, check
+them, allocate the outputs and run on the tensors' device and torch's current
+stream.
 """
 from __future__ import annotations
 
@@ -30,8 +32,12 @@ def _library():
         lib.trsm_linrec_backward.argtypes = [i32, i32, i64, i64, i64, *rows, *rows, *rows, vp, i64, *rows, vp, vp,
                                              *rows, *rows, vp, vp]
         lib.trsm_linrec_step.argtypes = [i32, i32, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp]
-        for fn in (lib.trsm_linrec_forward, lib.trsm_linrec_backward, lib.trsm_linrec_step):
+        sz = ctypes.c_size_t
+        lib.trsm_orthogonalize.argtypes = [i32, i32, i64, i64, *rows, *rows, i64, i64, vp, ctypes.c_double, vp, sz, vp]
+        for fn in (lib.trsm_linrec_forward, lib.trsm_linrec_backward, lib.trsm_linrec_step, lib.trsm_orthogonalize):
             fn.restype = i32
+        lib.trsm_orthogonalize_workspace_bytes.argtypes = [i32, i64, i64, i64, i64]
+        lib.trsm_orthogonalize_workspace_bytes.restype = sz
         _typed = lib
     return _typed
 
@@ -71,6 +77,35 @@ def trsm_linrec_step(dtype, form, batch, D, gate, gate_stride, x, x_stride, slot
     _check("trsm_linrec_step", _library().trsm_linrec_step(
         _code(ELEMS, dtype, "dtype"), _code(FORMS, form, "form"), batch, D, _ptr(gate), gate_stride, _ptr(x), x_stride,
         _ptr(slots), nslots, _ptr(state), state_stride, _ptr(next), next_stride, _ptr(y), y_stride, _stream(stream)))
+
+
+def _coefficients(steps, coef):
+    """A host array of 3 * steps doubles from one triple, or one per step; None
+    keeps the library's."""
+    if coef is None:
+        return None
+    flat = [float(v) for t in coef for v in (t if hasattr(t, "__len__") else (t,))]
+    if len(flat) == 3:
+        flat = flat * steps
+    if len(flat) != 3 * steps:
+        raise ValueError(f"coefficients: three numbers, or three for each of {steps} steps; got {len(flat)}")
+    return (ctypes.c_double * (3 * steps))(*flat)
+
+
+def trsm_orthogonalize(in_dtype, out_dtype, m, n, G, ldg, strideG, O, ldo, strideO, batch, steps=5, coef=None, eps=1e-7,
+                       workspace=None, ws_bytes=0, stream=None) -> None:
+    """Newton-Schulz orthogonalisation of row-major matrices (see
+    include/trsm_model.h); coef: (a, b, c), or one such triple per step."""
+    _check("trsm_orthogonalize", _library().trsm_orthogonalize(
+        _code(ELEMS, in_dtype, "in_dtype"), _code(ELEMS, out_dtype, "out_dtype"), m, n, _ptr(G), ldg, strideG, _ptr(O),
+        ldo, strideO, batch, steps, _coefficients(steps, coef), eps, _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def trsm_orthogonalize_workspace_bytes(in_dtype, m, n, batch, steps=5) -> int:
+    r = _library().trsm_orthogonalize_workspace_bytes(_code(ELEMS, in_dtype, "in_dtype"), m, n, batch, steps)
+    if r == ctypes.c_size_t(-1).value:
+        raise ValueError("trsm_orthogonalize_workspace_bytes: invalid arguments")
+    return int(r)
 
 
 # ------------------------------------------------------------------ torch tensors
@@ -292,3 +327,71 @@ def linear_recurrence_step(gate, x, state, *, form="decay", slots=None, out_stat
         state.shape[0], state.data_ptr(), state.stride(0), out_state.data_ptr(), out_state.stride(0), y.data_ptr(), D,
         st)))
     return y
+
+
+def _matrices(name, t):
+    """(row stride, matrix stride, transposed) of (..., m, n) matrices that
+    are row-major, or column-major: then of the transposed ones."""
+    m, n = t.shape[-2], t.shape[-1]
+    s0, s1 = t.stride(-2), t.stride(-1)
+    if (s1 == 1 or n == 1) and (s0 >= n or m == 1):
+        ld, flipped = max(s0, n), False
+    elif (s0 == 1 or m == 1) and (s1 >= m or n == 1):
+        ld, flipped = max(s1, m), True
+    else:
+        raise ValueError(f"{name}: each matrix must be row-major or column-major (unit stride in one dim)")
+    return ld, t.stride(0) if t.dim() == 3 else 0, flipped
+
+
+def orthogonalize(G, *, steps=5, coefficients=None, eps=1e-7, out=None):
+    """The matrix, or each of a batch (batch, m, n), brought towards the
+    nearest one with orthonormal rows (columns, where it is taller than wide)
+    by ``steps`` Newton-Schulz products X <- (a I + b S + c S^2) X, S = X X^T,
+    from X = G / (|G|_F + eps).
+
+    ``G`` is float32, float16 or bfloat16 on the GPU, each matrix row- or
+    column-major.  ``coefficients``: (a, b, c), or one triple per step; None
+    takes 3.4445, -4.7750, 2.0315, which brings singular values above 0.003 to
+    0.7 .. 1.2 in five steps.  Returns ``out`` (float16 or bfloat16, laid out
+    like G), or a new tensor: float16 for a float16 G, else bfloat16.
+    """
+    torch = _load_torch()
+    if not G.is_cuda:
+        raise ValueError("orthogonalize takes CUDA (device) tensors; got a CPU tensor")
+    code = _elem.get(G.dtype)
+    if code is None:
+        raise TypeError(f"G: {G.dtype} (float32, float16 or bfloat16)")
+    if G.dim() not in (2, 3):
+        raise ValueError("G: expected (m, n) or (batch, m, n)")
+    if not 0 <= steps <= 64:
+        raise ValueError(f"steps: {steps} (0 to 64)")
+    if out is None:
+        out = torch.empty(G.shape, dtype=torch.float16 if code == 1 else torch.bfloat16, device=G.device)
+        if G.numel() and _matrices("G", G)[2]:
+            out = torch.empty(G.mT.shape, dtype=out.dtype, device=G.device).mT
+    else:
+        if out.shape != G.shape:
+            raise ValueError(f"out: shape {tuple(out.shape)}, expected {tuple(G.shape)}")
+        if out.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError(f"out: {out.dtype} (float16 or bfloat16)")
+        if out.get_device() != G.get_device():
+            raise ValueError(f"out: on {out.device}, expected {G.device}")
+    coef = _coefficients(steps, coefficients)
+    if not G.numel():
+        return out
+    ldg, sg, flip = _matrices("G", G)
+    ldo, so, flip_out = _matrices("out", out)
+    m, n = G.shape[-2:]
+    if flip != flip_out:
+        if min(m, n) > 1:
+            raise ValueError("out: must be row-major where G is, and column-major where G is")
+        flip, ldg, ldo = False, n, n  # a single row or column is both
+        if any(t.shape[-1] > 1 and t.stride(-1) != 1 or t.shape[-2] > 1 and t.stride(-2) != n for t in (G, out)):
+            raise ValueError("out: must be row-major where G is, and column-major where G is")
+    if flip:
+        m, n = n, m
+    batch = G.shape[0] if G.dim() == 3 else 1
+    _check("trsm_orthogonalize", _on_device(G, lambda st: _library().trsm_orthogonalize(
+        code, _elem[out.dtype], m, n, G.data_ptr(), ldg, sg, out.data_ptr(), ldo, so, batch, steps, coef, eps, None, 0,
+        st)))
+    return out
