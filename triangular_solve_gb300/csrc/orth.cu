@@ -67,7 +67,7 @@ struct Squares {
 };
 
 constexpr int kNormThreads = 256;
-constexpr int kNormBlocks = 64;  // per matrix, at most
+constexpr int kNormBlocks = 512;  // per matrix, at most
 
 // Sum over a block's threads, in a fixed order; valid in thread 0.
 __device__ __forceinline__ double block_sum(double v) {
@@ -155,57 +155,79 @@ __device__ __forceinline__ void split(float x, __half &hi, __half &lo) {
     lo = __float2half_rn(x - __half2float(hi));
 }
 
+// Eight elements of a row of G from column j on, zero past column n.
+template <typename T>
+__device__ __forceinline__ void load_8(const T *row, int64_t j, int64_t n, bool vec, float (&g)[8]) {
+    if (vec && j + 8 <= n) {
+        alignas(16) T v[8];
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+            reinterpret_cast<uint4 *>(v)[k] = reinterpret_cast<const uint4 *>(row + j)[k];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[k] = to_f32<T>(v[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[k] = j + k < n ? to_f32<T>(row[j + k]) : 0.f;
+    }
+}
+
 // X_0 = 2^14 2^e G in f16 (head and tail), transposed for a tall G, in tiles
-// of 64 x 64 through shared memory; rho goes to rho[b].  With out != null
-// (no steps): O = 2^e rho G instead.
+// of 64 x 64, a few for each block; rho goes to rho[b].  With out != null (no
+// steps): O = 2^e rho G instead.
 template <typename T, bool TALL>
 __global__ void __launch_bounds__(256) convert_kernel(const Input in, const double *__restrict__ partial, int count,
                                                       double eps, const Halves x, float *__restrict__ rho, void *out,
                                                       int64_t ldo, int64_t strideO, int out_bf16) {
-    __shared__ float tile[64][65];
-    const int b = blockIdx.z, tid = threadIdx.x;
+    __shared__ float tile[TALL ? 64 : 1][65];
+    const int b = blockIdx.y, tid = threadIdx.x, u = tid / 8, v = tid % 8 * 8;
     const Scale sc = scale_of(partial + (int64_t)b * count, count, eps);
     const T *G = static_cast<const T *>(in.G) + b * in.stride;
-    // tile of X: rows i0.., columns j0..; G's element is (i, j), or (j, i) tall
-    const int64_t i0 = (int64_t)blockIdx.y * 64, j0 = (int64_t)blockIdx.x * 64;
-    if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0) rho[b] = sc.rho;
-    const float s14 = out ? 1.f : kScaleX;
+    if (tid == 0 && blockIdx.x == 0) rho[b] = sc.rho;
+    const int64_t across = (in.n + 63) / 64, tiles = across * ((in.m + 63) / 64);
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t i0 = t / across * 64, j0 = t % across * 64;  // of G
+        if (TALL) __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-        const int u = q * 4 + tid / 64, v = tid % 64;  // v along G's rows
-        const int64_t i = TALL ? i0 + v : i0 + u, j = TALL ? j0 + u : j0 + v;
-        float g = 0.f;
-        if (i < x.r && j < x.c) {
-            g = to_f32<T>(TALL ? G[j * in.ld + i] : G[i * in.ld + j]);
-            g = g * sc.up * sc.more * s14;
-        }
-        if (TALL) tile[v][u] = g;
-        else tile[u][v] = g;
-    }
-    __syncthreads();
-    if (out) {
+        for (int q = 0; q < 2; ++q) {
+            const int64_t i = i0 + u + 32 * q, j = j0 + v;
+            if (i >= in.m) continue;
+            float g[8];
+            load_8<T>(G + i * in.ld, j, in.n, in.vec, g);
+            if (out) {
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-            const int u = q * 4 + tid / 64, v = tid % 64;  // v along O's rows
-            const int64_t i = TALL ? i0 + v : i0 + u, j = TALL ? j0 + u : j0 + v;
-            if (i < x.r && j < x.c) {
-                const float o = (TALL ? tile[v][u] : tile[u][v]) * sc.rho;
-                const int64_t at = b * strideO + (TALL ? j * ldo + i : i * ldo + j);
-                if (out_bf16) static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(o);
-                else static_cast<__half *>(out)[at] = __float2half_rn(o);
+                for (int k = 0; k < 8; ++k) {
+                    if (j + k >= in.n) break;
+                    const float o = g[k] * sc.up * sc.more * sc.rho;
+                    const int64_t at = b * strideO + i * ldo + j + k;
+                    if (out_bf16) static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(o);
+                    else static_cast<__half *>(out)[at] = __float2half_rn(o);
+                }
+                continue;
             }
-        }
-        return;
-    }
-    // 8 halves a thread: 64 rows of 8 groups; the row's padding gets zeros
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int u = q * 32 + tid / 8, v = tid % 8 * 8;
-        const int64_t i = i0 + u, j = j0 + v;
-        if (i < x.r && j < x.ld) {
             alignas(16) __half hi[8], lo[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) split(tile[u][v + k], hi[k], lo[k]);
+            for (int k = 0; k < 8; ++k) {
+                g[k] = g[k] * sc.up * sc.more * kScaleX;
+                if (TALL) tile[u + 32 * q][v + k] = g[k];
+                else split(g[k], hi[k], lo[k]);
+            }
+            if (!TALL && j < x.ld) {
+                const int64_t at = b * x.stride + i * x.ld + j;
+                *reinterpret_cast<uint4 *>(x.hi + at) = *reinterpret_cast<const uint4 *>(hi);
+                if (x.lo) *reinterpret_cast<uint4 *>(x.lo + at) = *reinterpret_cast<const uint4 *>(lo);
+            }
+        }
+        if (!TALL || out) continue;
+        __syncthreads();
+        // X's row is G's column; rows of the tile past m hold leftovers, which
+        // only reach the padding of X's rows
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int64_t i = j0 + u + 32 * q, j = i0 + v;  // of X
+            if (i >= x.r || j >= x.ld) continue;
+            alignas(16) __half hi[8], lo[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) split(tile[v + k][u + 32 * q], hi[k], lo[k]);
             const int64_t at = b * x.stride + i * x.ld + j;
             *reinterpret_cast<uint4 *>(x.hi + at) = *reinterpret_cast<const uint4 *>(hi);
             if (x.lo) *reinterpret_cast<uint4 *>(x.lo + at) = *reinterpret_cast<const uint4 *>(lo);
@@ -225,41 +247,52 @@ struct ProductArgs {
     float alpha;                  // factor of the sums (kGram, kApply, kFinish: times rho's power)
     float beta, diag;             // kPoly: plus beta S plus diag I
     const float *rho;             // per matrix, or null
-    const __half *S;
-    __half *out, *out_lo;         // out_lo: tail, or null
-    int64_t ld, stride;           // of S, out and out_lo
-    void *O;                      // kFinish
+    int tail;                     // kApply: the result's tail goes out too
+    int transposed, bf16;         // kFinish
+    void *O;                      // kFinish: stored element by element; null: through the maps
     int64_t ldo, strideO;
-    int transposed, bf16, vec;    // of O; vec: its rows take 16-byte stores
     int *status;
 };
 
+// out: the output in boxes of 32 rows x 64 columns (128-byte swizzle).
+// second: kApply the tail's likewise; symmetric or transposed, the output in
+// boxes of 64 rows x 32 columns.  in: kPoly, S as `out`.
 struct Maps {
-    CUtensorMap a, b_hi, b_lo;
+    CUtensorMap a, b_hi, b_lo, out, second, in;
 };
 
 constexpr int kTileM = 256, kBK = 64;
 constexpr uint32_t kABytes = 128 * kBK * 2;  // 128 rows of A per CTA
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kBox = 32 * 64 * 2;       // bytes of a box of the output
 
 template <int BN> struct Ring {
     static constexpr uint32_t kBBytes = BN / 2 * kBK * 2;  // half of B's columns per CTA
     static constexpr uint32_t kStage = kABytes + kBBytes;
-    static constexpr int kStages = BN == 256 ? 6 : 8;
-    static constexpr uint32_t kBars = 8u * (2 * kStages + 5);
-    static constexpr size_t kSmem = 1024 + kStages * kStage + 256;
-    static_assert(kBars + 4 <= 256, "barriers and the TMEM address fit their region");
+    static constexpr int kStages = BN == 256 ? 5 : 6;
+    static constexpr uint32_t kOut = kStages * kStage;     // output boxes: 2 by turns x 2 for each of 4 warps
+    static constexpr uint32_t kBars = kOut + 16 * kBox;
+    static constexpr uint32_t kTmem = kBars + 8u * (2 * kStages + 5 + 8);
+    static constexpr size_t kSmem = 1024 + kBars + 256;
+    static_assert(kTmem + 4 <= kBars + 256 && kSmem <= 227 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ uint32_t pack_half(float x, float y) {
     const __half2 h = __floats2half2_rn(x, y);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+__device__ __forceinline__ uint32_t pack_out(float x, float y, bool bf16) {
+    if (!bf16) return pack_half(x, y);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
 
 // A persistent kernel on CTA pairs; each pair takes 256 x BN tiles of the
-// output in turn.  Warp 0 loads (TMA, a ring of kStages slabs of K = 64),
-// warp 1 of the even CTA issues the MMAs, warps 2..5 empty the accumulators
-// (two in TMEM, so a tile's stores run under the next one's MMAs).
+// output in turn.  Warp 0 loads (TMA, a ring of slabs of K = 64), warp 1 of
+// the even CTA issues the MMAs, warps 2..5 empty the accumulators (two in
+// TMEM, so a tile's way out runs under the next one's MMAs): 64 columns at a
+// time through shared memory, from where TMA stores them, rows whole, and
+// for a symmetric product below the diagonal once more transposed.
 //
 // B is Y^T for a K-major Y (kGram, kPoly; Y = A's matrix) or a K x N matrix
 // with contiguous N (kApply, kFinish; BMN).
@@ -270,13 +303,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;  // the swizzle's period
-    const uint32_t bars = base + R::kStages * R::kStage;
+    unsigned char *const smem = smem_raw + (base - raw);
+    const uint32_t bars = base + R::kBars;
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (R::kStages + s); };
     auto acc_full = [&](int a) { return bars + 8u * (2 * R::kStages + a); };
     auto acc_empty = [&](int a) { return bars + 8u * (2 * R::kStages + 2 + a); };
     const uint32_t drain = bars + 8u * (2 * R::kStages + 4);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem_raw + (bars - raw) + R::kBars);
+    auto s_full = [&](int w, int k) { return bars + 8u * (2 * R::kStages + 5 + 2 * w + k); };  // kPoly: S has come
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + R::kTmem);
     __shared__ int abort_flag;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -320,6 +355,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
             mbar_init(acc_empty(a), 8);  // four warps in each CTA
         }
         mbar_init(drain, 1);
+        for (int w = 0; w < 4; ++w)
+            for (int k = 0; k < 2; ++k) mbar_init(s_full(w, k), 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 1) tc5::alloc_pair(smem_u32(tmem_slot), kTmemCols);
@@ -406,123 +443,146 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
         }
     } else {
         const int quarter = warp & 3;  // TMEM lanes 32 * quarter .. + 31
-        int i = 0;
-        for (int t = pair; t < g.tiles; t += npairs, ++i) {
+        // this warp's boxes, first and second of each turn
+        auto box = [&](int turn, int k) { return R::kOut + (uint32_t)(quarter * 4 + turn * 2 + k) * kBox; };
+        int i = 0, turns = 0, issued = 0;  // groups done; loads of S (lane 0)
+        bool ok = true;
+        for (int t = pair; t < g.tiles && ok; t += npairs, ++i) {
             const int a = i & 1;
             int z, tm, tn;
             tile_of(t, z, tm, tn);
-            const int row = tm * kTileM + 128 * (int)rank + 32 * quarter + lane, col0 = tn * BN;
-            const bool row_ok = row < g.M;
-            const int64_t at = z * g.stride + (int64_t)row * g.ld;
+            const int row0 = tm * kTileM + 128 * (int)rank + 32 * quarter, row = row0 + lane, col0 = tn * BN;
+            // 64-column groups of this warp inside the output
+            const int groups = row0 >= g.M ? 0 : min(BN / 64, (g.N - col0 + 63) / 64);
+            const bool mirror = g.symmetric && col0 + BN <= tm * kTileM;  // below the diagonal tile
             float alpha = g.alpha;
             if (g.rho) alpha *= g.mode == kGram ? g.rho[z] * g.rho[z] : g.rho[z];
+            auto fetch_s = [&](int q, int turn) {  // lane 0: S's box q into the turn's first box
+                const uint32_t bar = s_full(quarter, turn & 1);
+                mbar_expect_tx(bar, kBox);
+                tma_load_3d(base + box(turn & 1, 0), &maps.in, col0 + 64 * q, row0, z, bar);
+                ++issued;
+            };
+            if (g.mode == kPoly && groups && lane == 0) {
+                bulk_wait_read<1>();  // the box's last store, two groups ago
+                fetch_s(0, turns);
+            }
             if (!mbar_wait(acc_full(a), (i >> 1) & 1)) {
                 if (lane == 0) fail();
-                break;
+                ok = false;
             }
-            if (aborted()) break;
+            ok = __all_sync(~0u, ok && !aborted());
             tc5::fence_after();
             const uint32_t addr = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(a * 256);
 #pragma unroll 1
-            for (int chunk = 0; chunk < BN / 32; ++chunk) {
-                const int col = col0 + chunk * 32;
-                uint32_t v[32];
-                tc5::read_32(v, addr + chunk * 32);
-                if (chunk + 1 == BN / 32) {
-                    tc5::fence_before();
+            for (int q = 0; q < groups && ok; ++q, ++turns) {
+                const int k = turns & 1;
+                const int col = col0 + 64 * q;
+                unsigned char *const first = smem + box(k, 0), *const second = smem + box(k, 1);
+                if (g.mode == kPoly) {
+                    if (lane == 0 && q + 1 < groups) {
+                        bulk_wait_read<0>();  // the other box's last store, the group before
+                        fetch_s(q + 1, turns + 1);
+                    }
+                    ok = __all_sync(~0u, mbar_wait(s_full(quarter, k), (turns >> 1) & 1));
+                    if (!ok) {
+                        if (lane == 0) fail();
+                        break;
+                    }
+                } else {
+                    // the boxes' last stores, two groups ago, have been read
+                    if (lane == 0) bulk_wait_read<1>();
                     __syncwarp();
-                    if (lane == 0) tc5::arrive_cluster(cluster::map(acc_empty(a), 0));
                 }
-                if (!row_ok || col >= g.N) continue;
-                if (g.mode == kFinish) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t v[32];
+                    tc5::read_32(v, addr + 64 * q + 32 * half);
                     float o[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) o[j] = alpha * __uint_as_float(v[j]);
-                    const int64_t zo = z * g.strideO;
-                    auto put = [&](int64_t p, float x) {
-                        if (g.bf16) static_cast<__nv_bfloat16 *>(g.O)[p] = __float2bfloat16_rn(x);
-                        else static_cast<__half *>(g.O)[p] = __float2half_rn(x);
+                    // 16-byte piece p of this thread's row, under the swizzle
+                    auto piece = [&](unsigned char *b, int p) {
+                        return reinterpret_cast<uint4 *>(b + lane * 128 + ((4 * half + p) ^ (lane & 7)) * 16);
                     };
-                    if (g.transposed) {
+                    if (g.mode == kPoly) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (col + j < g.N) put(zo + (int64_t)(col + j) * g.ldo + row, o[j]);
-                    } else if (g.vec && col + 32 <= g.N) {
-                        uint32_t w[16];
+                        for (int p = 0; p < 4; ++p) {
+                            const uint4 w = *piece(first, p);
+                            const __half *h = reinterpret_cast<const __half *>(&w);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                o[8 * p + j] = fmaf(g.beta, __half2float(h[j]), o[8 * p + j]);
+                                if (col + 32 * half + 8 * p + j == row) o[8 * p + j] += g.diag;
+                            }
+                        }
+                    }
+                    if (g.mode == kFinish && g.O) {
+                        const int64_t zo = z * g.strideO;
+                        auto put = [&](int64_t at, float x) {
+                            if (g.bf16) static_cast<__nv_bfloat16 *>(g.O)[at] = __float2bfloat16_rn(x);
+                            else static_cast<__half *>(g.O)[at] = __float2half_rn(x);
+                        };
+                        if (row < g.M) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const int64_t c = col + 32 * half + j;
+                                if (c < g.N) put(zo + (g.transposed ? c * g.ldo + row : row * g.ldo + c), o[j]);
+                            }
+                        }
+                        continue;
+                    }
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) w[j] = pack_out(o[2 * j], o[2 * j + 1], g.mode == kFinish && g.bf16);
+                    if (!(g.mode == kFinish && g.transposed)) {
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)
+                            *piece(first, p) = make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
+                    }
+                    if (mirror || (g.mode == kFinish && g.transposed)) {
+                        // column j of the warp's rows as row j of the second box
+                        uint16_t *b = reinterpret_cast<uint16_t *>(second) + 32 * half * 32 + lane;
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            if (g.bf16) {
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * j], o[2 * j + 1]);
-                                w[j] = *reinterpret_cast<const uint32_t *>(&h);
-                            } else {
-                                w[j] = pack_half(o[2 * j], o[2 * j + 1]);
+                            b[(2 * j) * 32] = (uint16_t)w[j];
+                            b[(2 * j + 1) * 32] = (uint16_t)(w[j] >> 16);
+                        }
+                    } else if (g.tail) {
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            uint32_t lo[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const __half2 hi = *reinterpret_cast<const __half2 *>(&w[4 * p + j]);
+                                lo[j] = pack_half(o[8 * p + 2 * j] - __low2float(hi),
+                                                  o[8 * p + 2 * j + 1] - __high2float(hi));
                             }
+                            *piece(second, p) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                         }
-                        uint4 *p = reinterpret_cast<uint4 *>(static_cast<__half *>(g.O) + zo + (int64_t)row * g.ldo + col);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) p[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (col + j < g.N) put(zo + (int64_t)row * g.ldo + col + j, o[j]);
                     }
-                    continue;
                 }
-                if (g.symmetric && col > row) continue;
-                float o[32];
-                if (g.mode == kPoly) {
-                    const __half *s = g.S + at + col;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint4 w = make_uint4(0, 0, 0, 0);
-                        if (col + 8 * q < g.ld) w = *reinterpret_cast<const uint4 *>(s + 8 * q);
-                        const __half *h = reinterpret_cast<const __half *>(&w);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            o[8 * q + j] = fmaf(g.beta, __half2float(h[j]), alpha * __uint_as_float(v[8 * q + j]));
-                            if (col + 8 * q + j == row) o[8 * q + j] += g.diag;
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = alpha * __uint_as_float(v[j]);
-                }
-                if (!g.symmetric) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (col + 8 * q < g.ld) {  // the row's padding gets the zeros beyond N
-                            alignas(16) __half hi[8], lo[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) split(o[8 * q + j], hi[j], lo[j]);
-                            *reinterpret_cast<uint4 *>(g.out + at + col + 8 * q) = *reinterpret_cast<const uint4 *>(hi);
-                            if (g.out_lo)
-                                *reinterpret_cast<uint4 *>(g.out_lo + at + col + 8 * q) =
-                                    *reinterpret_cast<const uint4 *>(lo);
-                        }
-                    }
-                } else {
-                    // the part on and below the diagonal, and its mirror image
-                    __half *out = g.out + z * g.stride;
-                    if (col + 31 <= row) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            *reinterpret_cast<uint4 *>(out + (int64_t)row * g.ld + col + 8 * q) = make_uint4(
-                                pack_half(o[8 * q], o[8 * q + 1]), pack_half(o[8 * q + 2], o[8 * q + 3]),
-                                pack_half(o[8 * q + 4], o[8 * q + 5]), pack_half(o[8 * q + 6], o[8 * q + 7]));
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) out[(int64_t)(col + j) * g.ld + row] = __float2half_rn(o[j]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            if (col + j <= row) {
-                                const __half h = __float2half_rn(o[j]);
-                                out[(int64_t)row * g.ld + col + j] = h;
-                                out[(int64_t)(col + j) * g.ld + row] = h;
-                            }
-                        }
-                    }
+                if (g.mode == kFinish && g.O) continue;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (!(g.mode == kFinish && g.transposed)) tma_store_3d(&maps.out, col, row0, z, base + box(k, 0));
+                    if (mirror || (g.mode == kFinish && g.transposed))
+                        tma_store_3d(&maps.second, row0, col, z, base + box(k, 1));
+                    else if (g.tail) tma_store_3d(&maps.second, col, row0, z, base + box(k, 1));
+                    bulk_commit();
                 }
             }
+            // every TMEM read of accumulator a is done: hand it back
+            tc5::fence_before();
+            __syncwarp();
+            if (lane == 0) tc5::arrive_cluster(cluster::map(acc_empty(a), 0));
+        }
+        if (lane == 0) {
+            bulk_wait<0>();
+            // given up: loads of S in flight land before shared memory goes away
+            for (; turns < issued; ++turns)
+                if (!mbar_wait(s_full(quarter, turns & 1), (turns >> 1) & 1)) record_timeout(g.status);
         }
     }
     tc5::fence_before();
@@ -566,14 +626,19 @@ struct Layout {
         lds = up8(r);
         x = (size_t)round256(batch * r * ldx * 2);
         s = (size_t)round256(batch * r * lds * 2);
-        partial = (size_t)round256(batch * kNormBlocks * 8);
+        partial = (size_t)round256(batch * norm_blocks(m, n) * 8);
         rho = (size_t)round256(batch * 4);
     }
     size_t total() const { return 4 * x + 2 * s + partial + rho; }
 };
 
-int make_map(CUtensorMap *map, const __half *p, int64_t inner, int64_t rows, int64_t batch, int64_t ld, int64_t stride,
-             int box_inner, int box_rows) {
+// An f16 (or 16-bit) matrix per batch entry, inner x rows; ld and stride in elements.
+struct Matrix {
+    const void *p;
+    int64_t inner, rows, ld, stride;
+};
+
+int make_map(CUtensorMap *map, const Matrix &x, int64_t batch, int box_inner, int box_rows, bool swizzled = true) {
     static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -583,11 +648,12 @@ int make_map(CUtensorMap *map, const __half *p, int64_t inner, int64_t rows, int
         return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }();
     if (!encode) return TRSM_ERR_CUDA_BASE + (int)cudaErrorNotSupported;
-    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)batch};
-    const cuuint64_t strides[2] = {(cuuint64_t)(ld * 2), (cuuint64_t)(stride * 2)};
+    const cuuint64_t dims[3] = {(cuuint64_t)x.inner, (cuuint64_t)x.rows, (cuuint64_t)batch};
+    const cuuint64_t strides[2] = {(cuuint64_t)(x.ld * 2), (cuuint64_t)(x.stride * 2)};
     const cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, 1}, one[3] = {1, 1, 1};
-    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half *>(p), dims, strides, box, one,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(x.p), dims, strides, box, one,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? TRSM_SUCCESS : TRSM_ERR_CUDA_BASE + (int)cudaErrorInvalidValue;
 }
@@ -605,37 +671,9 @@ int sm_count(int *out) {
     return TRSM_SUCCESS;
 }
 
-// One operand: an f16 matrix per batch entry, inner x rows, ld and stride in halves.
-struct Operand {
-    const __half *hi, *lo;
-    int64_t inner, rows, ld, stride;
-};
-
 template <int BN, bool BMN>
-int launch_product(const Operand &A, const Operand &B, ProductArgs g, cudaStream_t st) {
+int launch_product(const Maps &maps, const ProductArgs &g, int sms, cudaStream_t st) {
     using R = Ring<BN>;
-    Maps maps;
-    int rc = make_map(&maps.a, A.hi, A.inner, A.rows, g.batch, A.ld, A.stride, kBK, 128);
-    const int bi = BMN ? 64 : kBK, br = BMN ? kBK : BN / 2;
-    if (!rc) rc = make_map(&maps.b_hi, B.hi, B.inner, B.rows, g.batch, B.ld, B.stride, bi, br);
-    if (!rc) rc = make_map(&maps.b_lo, B.lo ? B.lo : B.hi, B.inner, B.rows, g.batch, B.ld, B.stride, bi, br);
-    int sms = 0;
-    if (!rc) rc = sm_count(&sms);
-    if (!rc) rc = device_status_word(&g.status);
-    if (rc) return rc;
-    g.halves = B.lo ? 2 : 1;
-    g.tiles_m = (g.M + kTileM - 1) / kTileM;
-    g.tiles_n = (g.N + BN - 1) / BN;
-    int64_t per = (int64_t)g.tiles_m * g.tiles_n;
-    if (g.symmetric) {
-        per = 0;
-        for (int tm = 0; tm < g.tiles_m; ++tm) {
-            const int w = kTileM / BN * (tm + 1);
-            per += w < g.tiles_n ? w : g.tiles_n;
-        }
-    }
-    if (per * g.batch > 0x7fffffff) return -11;
-    g.tiles = (int)(per * g.batch);
     cudaError_t e = cudaFuncSetAttribute(product_kernel<BN, BMN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)R::kSmem);
     if (e != cudaSuccess) return cuda_status(e);
@@ -644,12 +682,24 @@ int launch_product(const Operand &A, const Operand &B, ProductArgs g, cudaStream
     return launch_status();
 }
 
-template <bool BMN>
-int product(const Operand &A, const Operand &B, const ProductArgs &g, int sms, cudaStream_t st) {
+// The column tile of a product and its tiles, counted into g.
+int plan(ProductArgs &g, int sms, int *bn) {
     // 256 x 128 tiles while 256 x 256 ones would leave CTA pairs without one
     const int64_t wide = (int64_t)((g.M + 255) / 256) * ((g.N + 255) / 256) * g.batch;
-    if (g.N <= 128 || wide < sms / 2) return launch_product<128, BMN>(A, B, g, st);
-    return launch_product<256, BMN>(A, B, g, st);
+    *bn = g.N <= 128 || wide < sms / 2 ? 128 : 256;
+    g.tiles_m = (g.M + kTileM - 1) / kTileM;
+    g.tiles_n = (g.N + *bn - 1) / *bn;
+    int64_t per = (int64_t)g.tiles_m * g.tiles_n;
+    if (g.symmetric) {
+        per = 0;
+        for (int tm = 0; tm < g.tiles_m; ++tm) {
+            const int w = kTileM / *bn * (tm + 1);
+            per += w < g.tiles_n ? w : g.tiles_n;
+        }
+    }
+    if (per * g.batch > 0x7fffffff) return -11;
+    g.tiles = (int)(per * g.batch);
+    return TRSM_SUCCESS;
 }
 
 template <typename T>
@@ -658,7 +708,9 @@ int convert(const OrthArgs &a, const Input &in, const Halves &x, double *partial
     norm_kernel<T><<<dim3(nb, (unsigned)a.batch), kNormThreads, 0, st>>>(in, partial);
     int rc = launch_status();
     if (rc) return rc;
-    const dim3 grid((unsigned)((x.c + 63) / 64), (unsigned)((x.r + 63) / 64), (unsigned)a.batch);
+    // about 8 blocks for each SM (each computes the scale once)
+    const int64_t tiles = ((a.m + 63) / 64) * ((a.n + 63) / 64), most = (8 * 152 + a.batch - 1) / a.batch;
+    const dim3 grid((unsigned)(tiles < most ? tiles : most), (unsigned)a.batch);
     void *out = a.steps ? nullptr : a.O;
     if (a.m > a.n)
         convert_kernel<T, true><<<grid, 256, 0, st>>>(in, partial, nb, a.eps, x, rho, out, a.ldo, a.strideO,
@@ -697,62 +749,109 @@ int run(const OrthArgs &a, cudaStream_t st) {
         default: rc = convert<__nv_bfloat16>(a, in, x0, partial, rho, st); break;
     }
     if (!rc) rc = sm_count(&sms);
+    if (rc || !a.steps) return rc;
+
+    // The two shapes of product, and every tensor map that the steps use: each
+    // buffer in each part that it plays, by turns for X.
+    ProductArgs sym = {}, app = {};
+    sym.M = sym.N = app.M = (int)w.r;
+    app.N = (int)w.c;
+    app.K = (int)w.r;
+    sym.batch = app.batch = (int)a.batch;
+    sym.symmetric = 1;
+    int bn_sym, bn_app;
+    rc = plan(sym, sms, &bn_sym);
+    if (!rc) rc = plan(app, sms, &bn_app);
+    if (!rc) rc = device_status_word(&sym.status);
+    app.status = sym.status;
+    const Matrix mS = {S, w.r, w.r, w.lds, w.r * w.lds}, mC = {C, w.r, w.r, w.lds, w.r * w.lds};
+    Maps gram[2], poly, apply[2];
+    auto map = [&](CUtensorMap *m, const Matrix &x, int inner, int rows, bool swizzled = true) {
+        if (!rc) rc = make_map(m, x, a.batch, inner, rows, swizzled);
+    };
+    for (int k = 0; k < 2; ++k) {
+        const Matrix mX = {xh[k], w.c, w.r, w.ldx, w.r * w.ldx}, mL = {xl[k], w.c, w.r, w.ldx, w.r * w.ldx};
+        if (k && a.steps == 1) break;
+        // S = X X^T
+        map(&gram[k].a, mX, kBK, 128);
+        map(&gram[k].b_hi, mX, kBK, bn_sym / 2);
+        gram[k].b_lo = gram[k].b_hi;
+        if (k == 0) {
+            map(&gram[0].out, mS, 64, 32);
+            map(&gram[0].second, mS, 32, 64, false);
+        } else {
+            gram[1].out = gram[0].out;
+            gram[1].second = gram[0].second;
+        }
+        gram[k].in = gram[k].out;
+        // X = C X, from buffer k to the other
+        map(&apply[k].b_hi, mX, 64, kBK);
+        map(&apply[k].b_lo, mL, 64, kBK);
+        map(&apply[k ^ 1].out, mX, 64, 32);
+        map(&apply[k ^ 1].second, mL, 64, 32);
+    }
+    map(&poly.a, mS, kBK, 128);
+    map(&poly.b_hi, mS, kBK, bn_sym / 2);
+    poly.b_lo = poly.b_hi;
+    map(&poly.out, mC, 64, 32);
+    map(&poly.second, mC, 32, 64, false);
+    poly.in = gram[0].out;
+    map(&apply[0].a, mC, kBK, 128);
+    apply[1].a = apply[0].a;
+    // the last product writes O, by TMA where its rows start on 16-byte boundaries
+    Maps finish = apply[(a.steps - 1) & 1];
+    const bool tall = a.m > a.n;
+    uintptr_t ob = (uintptr_t)a.O;
+    if (a.m > 1) ob |= (uintptr_t)(a.ldo * 2);
+    if (a.batch > 1) ob |= (uintptr_t)(a.strideO * 2);
+    const bool direct = ob % 16 != 0;
+    if (!direct) {
+        // strides of a single row or matrix are of no account, but a map needs valid ones
+        const int64_t ld = a.m > 1 ? a.ldo : up8(a.n), so = a.batch > 1 ? a.strideO : up8(a.m * ld);
+        const Matrix mO = {a.O, a.n, a.m, ld, so};
+        map(tall ? &finish.second : &finish.out, mO, tall ? 32 : 64, tall ? 64 : 32, !tall);
+        if (tall) finish.out = finish.second;
+        else finish.second = finish.out;
+    }
+
     for (int k = 0; k < a.steps && !rc; ++k) {
         const double ca = a.coef[3 * k], cb = a.coef[3 * k + 1], cc = a.coef[3 * k + 2];
-        const int from = k & 1, to = from ^ 1;
-        const Operand X = {xh[from], tail ? xl[from] : nullptr, w.c, w.r, w.ldx, w.r * w.ldx};
-        const Operand Xhead = {X.hi, nullptr, X.inner, X.rows, X.ld, X.stride};
-        const Operand So = {S, nullptr, w.r, w.r, w.lds, w.r * w.lds}, Co = {C, nullptr, w.r, w.r, w.lds, w.r * w.lds};
-        ProductArgs g = {};
-        g.batch = (int)a.batch;
-        g.rho = k == 0 ? rho : nullptr;
-        // S = X X^T
-        g.M = g.N = (int)w.r;
-        g.K = (int)w.c;
-        g.symmetric = 1;
+        const int from = k & 1;
+        const bool last = k + 1 == a.steps;
+        ProductArgs g = sym;
         g.mode = kGram;
+        g.K = (int)w.c;
+        g.halves = 1;
+        g.rho = k == 0 ? rho : nullptr;
         g.alpha = kScaleS / (kScaleX * kScaleX);
-        g.out = S;
-        g.ld = w.lds;
-        g.stride = w.r * w.lds;
-        rc = product<false>(Xhead, Xhead, g, sms, st);
+        rc = bn_sym == 256 ? launch_product<256, false>(gram[from], g, sms, st)
+                           : launch_product<128, false>(gram[from], g, sms, st);
         if (rc) break;
-        // C = a I + b S + c S^2
-        g.K = (int)w.r;
         g.mode = kPoly;
+        g.K = (int)w.r;
         g.rho = nullptr;
         g.alpha = (float)cc / kScaleS;
         g.beta = (float)cb;
         g.diag = (float)ca * kScaleS;
-        g.S = S;
-        g.out = C;
-        rc = product<false>(So, So, g, sms, st);
+        rc = bn_sym == 256 ? launch_product<256, false>(poly, g, sms, st)
+                           : launch_product<128, false>(poly, g, sms, st);
         if (rc) break;
-        // X = C X
+        g = app;
+        g.mode = last ? kFinish : kApply;
+        g.halves = tail ? 2 : 1;
         g.rho = k == 0 ? rho : nullptr;
-        g.symmetric = 0;
-        g.N = (int)w.c;
-        g.alpha = 1.f / kScaleS;
-        g.ld = w.ldx;
-        g.stride = w.r * w.ldx;
-        if (k + 1 < a.steps) {
-            tail = has_tail(a.coef, a.steps, k + 1, exact);
-            g.mode = kApply;
-            g.out = xh[to];
-            g.out_lo = tail ? xl[to] : nullptr;
-        } else {
-            g.mode = kFinish;
-            g.alpha /= kScaleX;
-            g.O = a.O;
+        g.alpha = last ? 1.f / (kScaleS * kScaleX) : 1.f / kScaleS;
+        tail = !last && has_tail(a.coef, a.steps, k + 1, exact);
+        g.tail = tail;
+        if (last) {
+            g.transposed = tall;
+            g.bf16 = a.out_dtype == TRSM_ELEM_BF16;
+            g.O = direct ? a.O : nullptr;
             g.ldo = a.ldo;
             g.strideO = a.strideO;
-            g.transposed = a.m > a.n;
-            g.bf16 = a.out_dtype == TRSM_ELEM_BF16;
-            uintptr_t ob = (uintptr_t)a.O | (uintptr_t)(a.ldo * 2);
-            if (a.batch > 1) ob |= (uintptr_t)(a.strideO * 2);
-            g.vec = ob % 16 == 0;
         }
-        rc = product<true>(Co, X, g, sms, st);
+        const Maps &m = last ? finish : apply[from];
+        rc = bn_app == 256 ? launch_product<256, true>(m, g, sms, st) : launch_product<128, true>(m, g, sms, st);
     }
     return rc;
 }
