@@ -163,7 +163,10 @@ int trsm_orthogonalize(trsm_elem_t in_dtype, trsm_elem_t out_dtype, int64_t m, i
                        int64_t strideG, void *O, int64_t ldo, int64_t strideO, int64_t batch, int64_t steps,
                        const double *coef, double eps, void *workspace, size_t ws_bytes, void *stream);
 
-/* Workspace of trsm_orthogonalize in bytes; (size_t)-1 for invalid arguments. */
+/*
+ * Workspace of trsm_orthogonalize in bytes: 0 for small matrices (they stay
+ * on chip); (size_t)-1 for invalid arguments.
+ */
 size_t trsm_orthogonalize_workspace_bytes(trsm_elem_t in_dtype, int64_t m, int64_t n, int64_t batch, int64_t steps);
 
 #ifdef __cplusplus

@@ -72,7 +72,8 @@ def errors(got, want):
 
 
 SHAPES = [(1, 1, 1), (2, 1, 500), (2, 500, 1), (3, 2, 3), (4, 17, 5), (5, 64, 64), (3, 65, 64), (2, 100, 1001),
-          (1, 256, 257), (2, 300, 130), (1, 513, 700), (1, 1000, 384), (40, 32, 48), (3, 128, 128), (2, 129, 128)]
+          (1, 256, 257), (2, 300, 130), (1, 513, 700), (1, 1000, 384), (40, 32, 48), (3, 128, 128), (2, 129, 128),
+          (2, 31, 1200), (2, 33, 600), (2, 65, 240), (1, 128, 300), (1, 120, 320), (2, 1600, 20)]
 
 
 @pytest.mark.parametrize("name", ["f32", "f16", "bf16"])
@@ -185,7 +186,7 @@ def test_empty(env):
 
 def test_own_workspace(env):
     torch, tg = env
-    b, m, n = 2, 90, 130
+    b, m, n = 2, 190, 230
     G = torch.randn(b, m, n, device="cuda")
     want = tg.orthogonalize(G)
     need = tg.trsm_orthogonalize_workspace_bytes("f32", m, n, b)

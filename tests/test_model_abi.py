@@ -111,12 +111,15 @@ def test_orthogonalize_argument_errors_report_position(lib, pos, bad):
 
 def test_orthogonalize_workspace(lib):
     args = list(ORTH)
-    args[15] = tg.trsm_orthogonalize_workspace_bytes("bf16", 4, 6, 2) - 1
+    args[2:4], args[5], args[6], args[8], args[9] = (300, 200), 200, 60000, 200, 60000
+    args[15] = tg.trsm_orthogonalize_workspace_bytes("bf16", 300, 200, 2) - 1
+    assert args[15] > 4 * 2 * 300 * 200 * 2  # X twice, head and tail
     assert lib.trsm_orthogonalize(*args) == tg.ERR_WORKSPACE
     args[14], args[15] = FAKE + 8, 1 << 30
     assert lib.trsm_orthogonalize(*args) == tg.ERR_WORKSPACE
-    assert tg.trsm_orthogonalize_workspace_bytes("f32", 0, 6, 2) == 0
-    assert tg.trsm_orthogonalize_workspace_bytes("f32", 6, 4, 2) == tg.trsm_orthogonalize_workspace_bytes("f32", 4, 6, 2)
+    size = tg.trsm_orthogonalize_workspace_bytes
+    assert size("f32", 0, 300, 2) == 0 and size("f32", 64, 64, 1024) == 0  # nothing to do, on chip
+    assert size("f32", 300, 200, 2) == size("f32", 200, 300, 2)
     for bad in (dict(m=-1), dict(n=65537), dict(batch=-1), dict(steps=65)):
         with pytest.raises(ValueError):
             tg.trsm_orthogonalize_workspace_bytes(**(dict(in_dtype="f32", m=4, n=6, batch=1) | bad))

@@ -180,7 +180,7 @@ int trsm_orthogonalize(trsm_elem_t in_dtype, trsm_elem_t out_dtype, int64_t m, i
     if (m > 1 && ldo < n) return -9;
     if (batch > 1 && strideO < (m - 1) * ldo + n) return -10;
     const size_t need = orth_workspace_bytes((int)in_dtype, m, n, batch, steps);
-    if (workspace && (!good(workspace, 256) || ws_bytes < need)) return TRSM_ERR_WORKSPACE;
+    if (need && workspace && (!good(workspace, 256) || ws_bytes < need)) return TRSM_ERR_WORKSPACE;
     double defaults[3 * kMaxSteps];
     if (!coef) {
         for (int64_t k = 0; k < steps; ++k)
@@ -189,14 +189,15 @@ int trsm_orthogonalize(trsm_elem_t in_dtype, trsm_elem_t out_dtype, int64_t m, i
     }
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     void *ws = workspace;
-    if (!ws) {
+    const bool own = need && !workspace;
+    if (own) {
         const int rc = workspace_alloc(&ws, need, st);
         if (rc) return rc;
     }
     const OrthArgs a = {(int)in_dtype, (int)out_dtype, m, n, G, ldg, strideG, O, ldo, strideO, batch, (int)steps, coef,
                         eps, ws};
     int rc = orth_run(a, st);
-    if (!workspace) {
+    if (own) {
         const cudaError_t e = cudaFreeAsync(ws, st);
         if (!rc && e != cudaSuccess) rc = cuda_status(e);
     }

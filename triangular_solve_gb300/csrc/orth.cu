@@ -32,117 +32,62 @@
 #include "common.cuh"
 #include "internal.h"
 #include "orth.h"
+#include "orth_convert.cuh"
 #include "tcgen05.cuh"
 #include "trsm_model.h"
 
 namespace trsm {
 namespace orth {
 
-constexpr float kScaleX = 16384.f, kScaleS = 4096.f;  // 2^14, 2^12
-
-// ------------------------------------------------------------------ |G|_F and the f16 copy
-template <typename T> __device__ __forceinline__ float to_f32(T v);
-template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
-template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
-template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-// Sum of squares without overflow or underflow (J. L. Blue, "A portable
-// Fortran program to find the Euclidean norm of a vector", ACM TOMS 4(1),
-// 1978): large and small values are squared scaled, each kind on its own.
-struct Squares {
-    float big = 0.f, mid = 0.f, small = 0.f;
-    __device__ __forceinline__ void add(float x) {
-        const float y = fabsf(x);
-        if (y > 0x1p48f || y < 0x1p-48f) {
-            const float b = x * 0x1p-75f, s = x * 0x1p75f;
-            if (y > 1.f) big = fmaf(b, b, big);
-            else small = fmaf(s, s, small);
-        } else {
-            mid = fmaf(x, x, mid);  // NaN too
-        }
-    }
-    __device__ __forceinline__ double total() const {
-        return (double)big * 0x1p150 + (double)mid + (double)small * 0x1p-150;
-    }
-};
-
 constexpr int kNormThreads = 256;
 constexpr int kNormBlocks = 512;  // per matrix, at most
 
-// Sum over a block's threads, in a fixed order; valid in thread 0.
-__device__ __forceinline__ double block_sum(double v) {
-    __shared__ double part[kNormThreads / 32];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_down_sync(~0u, v, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    if (threadIdx.x == 0)
-        for (int w = 1; w < kNormThreads / 32; ++w) v += part[w];
-    return v;
-}
-
-struct Input {
-    const void *G;
-    int64_t m, n, ld, stride;  // rows, columns as given
-    bool vec;                  // rows of 16-byte vectors
-};
-
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const Input in, double *__restrict__ partial) {
-    constexpr int kVec = 16 / sizeof(T);
     const T *G = static_cast<const T *>(in.G) + blockIdx.y * in.stride;
     Squares s;
-    // vectors (or elements) of the rows in turn, without a division in the loop
-    const int64_t per = in.vec ? in.n / kVec : in.n;
-    const int64_t first = (int64_t)blockIdx.x * kNormThreads + threadIdx.x, step = (int64_t)gridDim.x * kNormThreads;
+    // groups of 8 along the rows in turn, without a division in the loop
+    const int64_t per = (in.n + 7) / 8, step = (int64_t)gridDim.x * kNormThreads;
+    const int64_t first = (int64_t)blockIdx.x * kNormThreads + threadIdx.x;
     const int64_t drow = step / per, dcol = step % per;
     int64_t row = first / per, col = first % per;
-    while (row < in.m) {
-        if (in.vec) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(G + row * in.ld + col * kVec);
-            const T *v = reinterpret_cast<const T *>(&w);
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) s.add(to_f32<T>(v[k]));
-        } else {
-            s.add(to_f32<T>(G[row * in.ld + col]));
-        }
+    auto next = [&]() {
         row += drow;
         col += dcol;
         if (col >= per) {
             col -= per;
             ++row;
         }
+    };
+    if (in.vec && in.n % 8 == 0) {
+        constexpr int kLoads = sizeof(T) / 2;  // 16-byte loads of a group
+        while (row < in.m) {
+            uint4 w[4][kLoads];  // four groups in flight; zeros past the end
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint4 *p = reinterpret_cast<const uint4 *>(G + row * in.ld + col * 8);
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k) w[q][k] = row < in.m ? p[k] : make_uint4(0, 0, 0, 0);
+                next();
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = to_f32<T>(reinterpret_cast<const T *>(w[q])[k]);
+                s.add_8(v);
+            }
+        }
+    } else {
+        while (row < in.m) {
+            float v[8];
+            load_8<T>(G + row * in.ld, col * 8, in.n, in.vec, v);
+            s.add_8(v);
+            next();
+        }
     }
     const double t = block_sum(s.total());
     if (threadIdx.x == 0) partial[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = t;
-}
-
-// 1 / (|G|_F + eps) as 2^e rho, rho in [1, 2); NaN where it is no positive
-// number.  Called by a whole block; every thread gets the same.
-struct Scale {
-    float up, more, rho;  // 2^e = up * more, neither of which overflows
-};
-__device__ __forceinline__ Scale scale_of(const double *partial, int count, double eps) {
-    __shared__ Scale shared;
-    if (threadIdx.x < 32) {
-        double sum = 0;
-        for (int i = threadIdx.x; i < count; i += 32) sum += partial[i];
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_down_sync(~0u, sum, o);
-        if (threadIdx.x == 0) {
-            const double s = 1.0 / (sqrt(sum) + eps);
-            if (s > 0 && s < 1e300) {
-                int e = ilogb(s);
-                const float rho = (float)scalbn(s, -e);
-                e = min(max(e, -160), 240);
-                shared = {scalbnf(1.f, e / 2), scalbnf(1.f, e - e / 2), rho};
-            } else {
-                shared = {1.f, 1.f, __int_as_float(0x7fffffff)};
-            }
-        }
-    }
-    __syncthreads();
-    return shared;
 }
 
 struct Halves {
@@ -150,39 +95,23 @@ struct Halves {
     int64_t r, c, ld, stride;
 };
 
-__device__ __forceinline__ void split(float x, __half &hi, __half &lo) {
-    hi = __float2half_rn(x);
-    lo = __float2half_rn(x - __half2float(hi));
-}
-
-// Eight elements of a row of G from column j on, zero past column n.
-template <typename T>
-__device__ __forceinline__ void load_8(const T *row, int64_t j, int64_t n, bool vec, float (&g)[8]) {
-    if (vec && j + 8 <= n) {
-        alignas(16) T v[8];
-#pragma unroll
-        for (int k = 0; k < (int)sizeof(T) / 2; ++k)
-            reinterpret_cast<uint4 *>(v)[k] = reinterpret_cast<const uint4 *>(row + j)[k];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] = to_f32<T>(v[k]);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] = j + k < n ? to_f32<T>(row[j + k]) : 0.f;
-    }
-}
-
 // X_0 = 2^14 2^e G in f16 (head and tail), transposed for a tall G, in tiles
 // of 64 x 64, a few for each block; rho goes to rho[b].  With out != null (no
-// steps): O = 2^e rho G instead.
+// steps): O = 2^e rho G instead.  done: the counters of the products, to zero.
 template <typename T, bool TALL>
 __global__ void __launch_bounds__(256) convert_kernel(const Input in, const double *__restrict__ partial, int count,
-                                                      double eps, const Halves x, float *__restrict__ rho, void *out,
-                                                      int64_t ldo, int64_t strideO, int out_bf16) {
+                                                      double eps, const Halves x, float *__restrict__ rho,
+                                                      unsigned *__restrict__ done, void *out, int64_t ldo,
+                                                      int64_t strideO, int out_bf16) {
     __shared__ float tile[TALL ? 64 : 1][65];
     const int b = blockIdx.y, tid = threadIdx.x, u = tid / 8, v = tid % 8 * 8;
     const Scale sc = scale_of(partial + (int64_t)b * count, count, eps);
     const T *G = static_cast<const T *>(in.G) + b * in.stride;
-    if (tid == 0 && blockIdx.x == 0) rho[b] = sc.rho;
+    if (tid == 0 && blockIdx.x == 0) {
+        rho[b] = sc.rho;
+        done[b] = 0;
+        if (b == 0) done[gridDim.y] = 0;  // the abort word
+    }
     const int64_t across = (in.n + 63) / 64, tiles = across * ((in.m + 63) / 64);
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         const int64_t i0 = t / across * 64, j0 = t % across * 64;  // of G
@@ -236,23 +165,7 @@ __global__ void __launch_bounds__(256) convert_kernel(const Input in, const doub
 }
 
 // ------------------------------------------------------------------ products
-enum Mode { kGram, kPoly, kApply, kFinish };
-
-struct ProductArgs {
-    int M, N, K, batch;
-    int tiles_m, tiles_n, tiles;  // of one matrix; all
-    int symmetric;                // only tiles that reach the diagonal or below
-    int halves;                   // B head only (1) or head and tail (2)
-    Mode mode;
-    float alpha;                  // factor of the sums (kGram, kApply, kFinish: times rho's power)
-    float beta, diag;             // kPoly: plus beta S plus diag I
-    const float *rho;             // per matrix, or null
-    int tail;                     // kApply: the result's tail goes out too
-    int transposed, bf16;         // kFinish
-    void *O;                      // kFinish: stored element by element; null: through the maps
-    int64_t ldo, strideO;
-    int *status;
-};
+enum Kind { kGram, kPoly, kApply };  // S = X X^T, C = a I + b S + c S^2, X = C X
 
 // out: the output in boxes of 32 rows x 64 columns (128-byte swizzle).
 // second: kApply the tail's likewise; symmetric or transposed, the output in
@@ -261,21 +174,41 @@ struct Maps {
     CUtensorMap a, b_hi, b_lo, out, second, in;
 };
 
+// Tiles of one kind of product: bn columns wide (128 or 256), per of them a
+// matrix.
+struct Tiling {
+    int bn, tiles_m, tiles_n, per;
+};
+
+// All products of a call.  Tiles are numbered step by step, product by
+// product and matrix by matrix.
+struct Schedule {
+    Maps gram[2], poly, apply[2], finish;  // by the buffer that holds X_k
+    Tiling sym, app;
+    int r, c, batch, steps, tiles;
+    int transposed, bf16;       // of O
+    void *O;                    // stored element by element; null: through the maps
+    int64_t ldo, strideO;
+    unsigned long long tails;   // bit k: X_k has a tail
+    const float *rho;           // per matrix
+    unsigned *done;             // per matrix: warps that have stored a tile; then the abort word
+    int *status;
+    float coef[3 * kMaxSteps];
+};
+
 constexpr int kTileM = 256, kBK = 64;
 constexpr uint32_t kABytes = 128 * kBK * 2;  // 128 rows of A per CTA
+constexpr uint32_t kStageBytes = 2 * kABytes;
+constexpr int kStages = 5;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kBox = 32 * 64 * 2;       // bytes of a box of the output
-
-template <int BN> struct Ring {
-    static constexpr uint32_t kBBytes = BN / 2 * kBK * 2;  // half of B's columns per CTA
-    static constexpr uint32_t kStage = kABytes + kBBytes;
-    static constexpr int kStages = BN == 256 ? 5 : 6;
-    static constexpr uint32_t kOut = kStages * kStage;     // output boxes: 2 by turns x 2 for each of 4 warps
-    static constexpr uint32_t kBars = kOut + 16 * kBox;
-    static constexpr uint32_t kTmem = kBars + 8u * (2 * kStages + 5 + 8);
-    static constexpr size_t kSmem = 1024 + kBars + 256;
-    static_assert(kTmem + 4 <= kBars + 256 && kSmem <= 227 * 1024, "shared memory");
-};
+constexpr uint32_t kOutAt = kStages * kStageBytes;  // output boxes: 2 by turns x 2 for each of 4 warps
+constexpr uint32_t kBarsAt = kOutAt + 16 * kBox;
+constexpr uint32_t kTmemAt = kBarsAt + 8u * (2 * kStages + 5 + 8);
+constexpr size_t kSmemBytes = 1024 + kBarsAt + 256;
+static_assert(kTmemAt + 4 <= kBarsAt + 256 && kSmemBytes <= 227 * 1024, "shared memory");
+constexpr int kPatience = 4;                 // full waits for what itself waits for another product
+constexpr unsigned kWarpsATile = 8;          // that store it: four in each CTA
 
 __device__ __forceinline__ uint32_t pack_half(float x, float y) {
     const __half2 h = __floats2half2_rn(x, y);
@@ -287,66 +220,112 @@ __device__ __forceinline__ uint32_t pack_out(float x, float y, bool bf16) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// A persistent kernel on CTA pairs; each pair takes 256 x BN tiles of the
-// output in turn.  Warp 0 loads (TMA, a ring of slabs of K = 64), warp 1 of
-// the even CTA issues the MMAs, warps 2..5 empty the accumulators (two in
-// TMEM, so a tile's way out runs under the next one's MMAs): 64 columns at a
-// time through shared memory, from where TMA stores them, rows whole, and
-// for a symmetric product below the diagonal once more transposed.
+// One tile of the schedule.
+struct Tile {
+    int step, kind, z, tm, tn;
+    unsigned before;  // warps' stores of this matrix's earlier products
+};
+__device__ __forceinline__ Tile tile_at(const Schedule &g, int t) {
+    const int sym = g.sym.per * g.batch, app = g.app.per * g.batch;
+    Tile x;
+    x.step = t / (2 * sym + app);
+    int u = t - x.step * (2 * sym + app);
+    x.kind = u < sym ? kGram : u < 2 * sym ? kPoly : kApply;
+    u -= x.kind * sym;
+    const Tiling &k = x.kind == kApply ? g.app : g.sym;
+    x.z = u / k.per;
+    u -= x.z * k.per;
+    x.before = kWarpsATile * (unsigned)(x.step * (2 * g.sym.per + g.app.per) + x.kind * g.sym.per);
+    if (x.kind != kApply) {
+        // row tile tm has the column tiles up to the diagonal's
+        const int more = kTileM / k.bn;
+        x.tm = 0;
+        int width = min(more, k.tiles_n);
+        while (u >= width) {
+            u -= width;
+            ++x.tm;
+            width = min(more * (x.tm + 1), k.tiles_n);
+        }
+        x.tn = u;
+    } else {
+        // groups of 8 row tiles, so that a wave shares its operands in L2
+        const int grp = u / (8 * k.tiles_n), rem = u - grp * 8 * k.tiles_n;
+        const int size = min(8, k.tiles_m - grp * 8);
+        x.tm = grp * 8 + rem % size;
+        x.tn = rem / size;
+    }
+    return x;
+}
+__device__ __forceinline__ const Maps &maps_of(const Schedule &g, const Tile &x) {
+    const int from = x.step & 1;
+    return x.kind == kGram ? g.gram[from] : x.kind == kPoly ? g.poly : x.step + 1 == g.steps ? g.finish : g.apply[from];
+}
+
+__device__ __forceinline__ unsigned load_acquire(const unsigned *p) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];\n" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+// Until `need` warps have stored their tiles of matrix z, with what they
+// stored visible to this thread's later TMA loads; false when the wait
+// expired or another CTA gave up.
+__device__ __forceinline__ bool wait_done(const Schedule &g, int z, unsigned need) {
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        if (load_acquire(g.done + z) >= need) {
+            asm volatile("fence.proxy.async;\n" ::: "memory");
+            return true;
+        }
+        if ((i & 63) == 63 && load_acquire(g.done + g.batch)) return false;
+    }
+    return false;
+}
+
+// The whole call in one persistent kernel on CTA pairs, one CTA an SM; each
+// pair takes 256 x bn tiles of the schedule in turn.  Warp 0 loads (TMA, a
+// ring of slabs of K = 64), warp 1 of the even CTA issues the MMAs, warps
+// 2..5 empty the accumulators (two in TMEM, so a tile's way out runs under
+// the next one's MMAs): 64 columns at a time through shared memory, from
+// where TMA stores them, rows whole, and for a symmetric product below the
+// diagonal once more transposed.
+//
+// A product waits for the one before it matrix by matrix: the warps that
+// store a tile count themselves in done[z] once their stores are complete,
+// and a tile's loads wait for the count of its matrix's earlier products.
+// Every tile comes after those it waits for, in the order in which each pair
+// takes its tiles, and the launch is cooperative, so the waits end; they are
+// bounded all the same.
 //
 // B is Y^T for a K-major Y (kGram, kPoly; Y = A's matrix) or a K x N matrix
-// with contiguous N (kApply, kFinish; BMN).
-template <int BN, bool BMN>
+// with contiguous N (kApply).
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
-    product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ProductArgs g) {
-    using R = Ring<BN>;
+    schedule_kernel(const __grid_constant__ Schedule g) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;  // the swizzle's period
     unsigned char *const smem = smem_raw + (base - raw);
-    const uint32_t bars = base + R::kBars;
+    const uint32_t bars = base + kBarsAt;
     auto full = [&](int s) { return bars + 8u * s; };
-    auto empty = [&](int s) { return bars + 8u * (R::kStages + s); };
-    auto acc_full = [&](int a) { return bars + 8u * (2 * R::kStages + a); };
-    auto acc_empty = [&](int a) { return bars + 8u * (2 * R::kStages + 2 + a); };
-    const uint32_t drain = bars + 8u * (2 * R::kStages + 4);
-    auto s_full = [&](int w, int k) { return bars + 8u * (2 * R::kStages + 5 + 2 * w + k); };  // kPoly: S has come
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + R::kTmem);
+    auto empty = [&](int s) { return bars + 8u * (kStages + s); };
+    auto acc_full = [&](int a) { return bars + 8u * (2 * kStages + a); };
+    auto acc_empty = [&](int a) { return bars + 8u * (2 * kStages + 2 + a); };
+    const uint32_t drain = bars + 8u * (2 * kStages + 4);
+    auto s_full = [&](int w, int k) { return bars + 8u * (2 * kStages + 5 + 2 * w + k); };  // kPoly: S has come
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kTmemAt);
     __shared__ int abort_flag;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster::rank();
     const bool leader = rank == 0;
     const int pair = (int)blockIdx.x >> 1, npairs = (int)gridDim.x >> 1;
-    const int nk = (g.K + kBK - 1) / kBK, slabs = nk * g.halves;
-    // tile t -> matrix z, row tile tm, column tile tn
-    auto tile_of = [&](int t, int &z, int &tm, int &tn) {
-        const int per = g.tiles / g.batch;
-        z = t / per;
-        int u = t % per;
-        if (g.symmetric) {
-            // row tile tm has the column tiles up to the diagonal's
-            constexpr int kPer = kTileM / BN;
-            tm = 0;
-            int width = min(kPer, g.tiles_n);
-            while (u >= width) {
-                u -= width;
-                ++tm;
-                width = min(kPer * (tm + 1), g.tiles_n);
-            }
-            tn = u;
-        } else {
-            // groups of 8 row tiles, so that a wave shares its operands in L2
-            const int grp = u / (8 * g.tiles_n), rem = u - grp * 8 * g.tiles_n;
-            const int size = min(8, g.tiles_m - grp * 8);
-            tm = grp * 8 + rem % size;
-            tn = rem / size;
-        }
+    // slabs of a tile: of the head, and in all
+    auto slabs_of = [&](const Tile &x, int &heads) {
+        heads = ((x.kind == kGram ? g.c : g.r) + kBK - 1) / kBK;
+        return x.kind == kApply && ((g.tails >> x.step) & 1) ? 2 * heads : heads;
     };
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
-        for (int s = 0; s < R::kStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
         }
@@ -368,6 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     auto aborted = [&]() { return *(volatile int *)&abort_flag != 0; };
     auto fail = [&]() {
         record_timeout(g.status);
+        atomicExch(g.done + g.batch, 1u);
         *(volatile int *)&abort_flag = 1;
     };
 
@@ -375,40 +355,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
         if (lane == 0) {
             int it = 0;
             for (int t = pair; t < g.tiles && !aborted(); t += npairs) {
-                int z, tm, tn;
-                tile_of(t, z, tm, tn);
-                const int ya = tm * kTileM + 128 * (int)rank, yb = tn * BN + BN / 2 * (int)rank;
+                const Tile x = tile_at(g, t);
+                const Maps &m = maps_of(g, x);
+                if (x.before && !wait_done(g, x.z, x.before)) {
+                    fail();
+                    break;
+                }
+                const bool bmn = x.kind == kApply;
+                const int bn = bmn ? g.app.bn : g.sym.bn;
+                const int ya = x.tm * kTileM + 128 * (int)rank, yb = x.tn * bn + bn / 2 * (int)rank;
+                int heads;
+                const int slabs = slabs_of(x, heads);
                 for (int kb = 0; kb < slabs; ++kb, ++it) {
-                    const int s = it % R::kStages;
-                    if (it >= R::kStages && !mbar_wait(empty(s), ((it / R::kStages) - 1) & 1)) {
+                    const int s = it % kStages;
+                    if (it >= kStages && !mbar_wait(empty(s), ((it / kStages) - 1) & 1)) {
                         fail();
                         break;
                     }
-                    if (leader) mbar_expect_tx(full(s), 2 * R::kStage);
-                    const uint32_t st = base + s * R::kStage, fb = cluster::map(full(s), 0);
-                    const int kx = kb % nk * kBK;
-                    const CUtensorMap *mb = kb < nk ? &maps.b_hi : &maps.b_lo;
-                    tc5::load_pair(st, &maps.a, kx, ya, z, fb);
-                    if constexpr (BMN) {
-#pragma unroll
-                        for (int q = 0; q < BN / 128; ++q)
-                            tc5::load_pair(st + kABytes + q * (64 * kBK * 2), mb, yb + 64 * q, kx, z, fb);
+                    if (leader) mbar_expect_tx(full(s), 2 * (kABytes + bn / 2 * kBK * 2));
+                    const uint32_t st = base + s * kStageBytes, fb = cluster::map(full(s), 0);
+                    const int kx = (kb < heads ? kb : kb - heads) * kBK;
+                    const CUtensorMap *mb = kb < heads ? &m.b_hi : &m.b_lo;
+                    tc5::load_pair(st, &m.a, kx, ya, x.z, fb);
+                    if (bmn) {
+                        for (int q = 0; q < bn / 128; ++q)
+                            tc5::load_pair(st + kABytes + q * (64 * kBK * 2), mb, yb + 64 * q, kx, x.z, fb);
                     } else {
-                        tc5::load_pair(st + kABytes, mb, kx, yb, z, fb);
+                        tc5::load_pair(st + kABytes, mb, kx, yb, x.z, fb);
                     }
                 }
             }
             if (aborted() && leader) {
                 // the pair's loads counted on these barriers land before shared memory goes away
-                for (int j = (it > R::kStages ? it - R::kStages : 0); j < it; ++j)
-                    if (!mbar_wait(full(j % R::kStages), (j / R::kStages) & 1)) record_timeout(g.status);
+                for (int j = (it > kStages ? it - kStages : 0); j < it; ++j)
+                    if (!mbar_wait(full(j % kStages), (j / kStages) & 1)) record_timeout(g.status);
             }
         }
     } else if (warp == 1) {
         if (lane == 0 && leader) {
-            constexpr uint32_t idesc = tc5::idesc_f16(kTileM, BN, BMN);
             int it = 0, i = 0;
             for (int t = pair; t < g.tiles && !aborted(); t += npairs, ++i) {
+                const Tile x = tile_at(g, t);
+                const bool bmn = x.kind == kApply;
+                const uint32_t idesc = tc5::idesc_f16(kTileM, bmn ? g.app.bn : g.sym.bn, bmn);
                 const int a = i & 1;
                 if (i >= 2 && !mbar_wait(acc_empty(a), ((i >> 1) - 1) & 1)) {
                     fail();
@@ -417,19 +406,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
                 tc5::fence_after();
                 const uint32_t d = tmem + (uint32_t)(a * 256);
                 bool ok = true;
+                int heads;
+                const int slabs = slabs_of(x, heads);
                 for (int kb = 0; kb < slabs; ++kb, ++it) {
-                    const int s = it % R::kStages;
-                    if (!mbar_wait(full(s), (it / R::kStages) & 1)) {
+                    const int s = it % kStages;
+                    // the loader may itself be waiting for an earlier product
+                    bool come = false;
+                    for (int tries = 0; tries < kPatience && !come && !aborted(); ++tries)
+                        come = mbar_wait(full(s), (it / kStages) & 1);
+                    if (!come) {
                         fail();
                         ok = false;
                         break;
                     }
                     tc5::fence_after();
-                    const uint32_t st = base + s * R::kStage;
+                    const uint32_t st = base + s * kStageBytes;
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk) {
                         const uint64_t da = tc5::desc_k_major(st + kk * 32);
-                        const uint64_t db = BMN ? tc5::desc_mn_major(st + kABytes + kk * 2048, 64 * kBK * 2)
+                        const uint64_t db = bmn ? tc5::desc_mn_major(st + kABytes + kk * 2048, 64 * kBK * 2)
                                                 : tc5::desc_k_major(st + kABytes + kk * 32);
                         tc5::mma_pair(d, da, db, idesc, kb != 0 || kk != 0);
                     }
@@ -444,31 +439,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     } else {
         const int quarter = warp & 3;  // TMEM lanes 32 * quarter .. + 31
         // this warp's boxes, first and second of each turn
-        auto box = [&](int turn, int k) { return R::kOut + (uint32_t)(quarter * 4 + turn * 2 + k) * kBox; };
-        int i = 0, turns = 0, issued = 0;  // groups done; loads of S (lane 0)
+        auto box = [&](int turn, int k) { return kOutAt + (uint32_t)(quarter * 4 + turn * 2 + k) * kBox; };
+        int i = 0, turns = 0;        // groups done
+        int loads = 0, issued = 0;   // boxes of S waited for; loaded (lane 0)
         bool ok = true;
         for (int t = pair; t < g.tiles && ok; t += npairs, ++i) {
             const int a = i & 1;
-            int z, tm, tn;
-            tile_of(t, z, tm, tn);
-            const int row0 = tm * kTileM + 128 * (int)rank + 32 * quarter, row = row0 + lane, col0 = tn * BN;
+            const Tile x = tile_at(g, t);
+            const Maps &maps = maps_of(g, x);
+            const int z = x.z, bn = x.kind == kApply ? g.app.bn : g.sym.bn, N = x.kind == kApply ? g.c : g.r;
+            const bool poly = x.kind == kPoly, finish = x.kind == kApply && x.step + 1 == g.steps;
+            const bool tail = x.kind == kApply && !finish && ((g.tails >> (x.step + 1)) & 1);
+            const bool out_bf16 = finish && g.bf16, turned = finish && g.transposed, plain = finish && g.O;
+            const int row0 = x.tm * kTileM + 128 * (int)rank + 32 * quarter, row = row0 + lane, col0 = x.tn * bn;
             // 64-column groups of this warp inside the output
-            const int groups = row0 >= g.M ? 0 : min(BN / 64, (g.N - col0 + 63) / 64);
-            const bool mirror = g.symmetric && col0 + BN <= tm * kTileM;  // below the diagonal tile
-            float alpha = g.alpha;
-            if (g.rho) alpha *= g.mode == kGram ? g.rho[z] * g.rho[z] : g.rho[z];
+            const int groups = row0 >= g.r ? 0 : min(bn / 64, (N - col0 + 63) / 64);
+            const bool mirror = x.kind != kApply && col0 + bn <= x.tm * kTileM;  // below the diagonal tile
+            const float rho = x.step == 0 ? g.rho[z] : 1.f;
+            const float beta = g.coef[3 * x.step + 1], diag = g.coef[3 * x.step] * kScaleS;
+            const float alpha = x.kind == kGram ? kScaleS / (kScaleX * kScaleX) * rho * rho
+                                : poly          ? g.coef[3 * x.step + 2] / kScaleS
+                                                : rho / kScaleS / (finish ? kScaleX : 1.f);
             auto fetch_s = [&](int q, int turn) {  // lane 0: S's box q into the turn's first box
-                const uint32_t bar = s_full(quarter, turn & 1);
+                const uint32_t bar = s_full(quarter, issued & 1);
                 mbar_expect_tx(bar, kBox);
                 tma_load_3d(base + box(turn & 1, 0), &maps.in, col0 + 64 * q, row0, z, bar);
                 ++issued;
             };
-            if (g.mode == kPoly && groups && lane == 0) {
-                bulk_wait_read<1>();  // the box's last store, two groups ago
-                fetch_s(0, turns);
+            bool come = true;
+            if (poly && groups && lane == 0) {
+                come = wait_done(g, z, x.before);
+                if (come) fetch_s(0, turns);
             }
-            if (!mbar_wait(acc_full(a), (i >> 1) & 1)) {
-                if (lane == 0) fail();
+            bool filled = false;
+            for (int tries = 0; tries < kPatience && !filled && !aborted(); ++tries)
+                filled = mbar_wait(acc_full(a), (i >> 1) & 1);
+            if (!filled || !come) {
+                fail();
                 ok = false;
             }
             ok = __all_sync(~0u, ok && !aborted());
@@ -479,12 +486,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
                 const int k = turns & 1;
                 const int col = col0 + 64 * q;
                 unsigned char *const first = smem + box(k, 0), *const second = smem + box(k, 1);
-                if (g.mode == kPoly) {
+                if (poly) {
                     if (lane == 0 && q + 1 < groups) {
                         bulk_wait_read<0>();  // the other box's last store, the group before
                         fetch_s(q + 1, turns + 1);
                     }
-                    ok = __all_sync(~0u, mbar_wait(s_full(quarter, k), (turns >> 1) & 1));
+                    ok = __all_sync(~0u, mbar_wait(s_full(quarter, loads & 1), (loads >> 1) & 1));
+                    ++loads;
                     if (!ok) {
                         if (lane == 0) fail();
                         break;
@@ -505,42 +513,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
                     auto piece = [&](unsigned char *b, int p) {
                         return reinterpret_cast<uint4 *>(b + lane * 128 + ((4 * half + p) ^ (lane & 7)) * 16);
                     };
-                    if (g.mode == kPoly) {
+                    if (poly) {
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
                             const uint4 w = *piece(first, p);
                             const __half *h = reinterpret_cast<const __half *>(&w);
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
-                                o[8 * p + j] = fmaf(g.beta, __half2float(h[j]), o[8 * p + j]);
-                                if (col + 32 * half + 8 * p + j == row) o[8 * p + j] += g.diag;
+                                o[8 * p + j] = fmaf(beta, __half2float(h[j]), o[8 * p + j]);
+                                if (col + 32 * half + 8 * p + j == row) o[8 * p + j] += diag;
                             }
                         }
                     }
-                    if (g.mode == kFinish && g.O) {
+                    if (plain) {
                         const int64_t zo = z * g.strideO;
                         auto put = [&](int64_t at, float x) {
                             if (g.bf16) static_cast<__nv_bfloat16 *>(g.O)[at] = __float2bfloat16_rn(x);
                             else static_cast<__half *>(g.O)[at] = __float2half_rn(x);
                         };
-                        if (row < g.M) {
+                        if (row < g.r) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j) {
                                 const int64_t c = col + 32 * half + j;
-                                if (c < g.N) put(zo + (g.transposed ? c * g.ldo + row : row * g.ldo + c), o[j]);
+                                if (c < N) put(zo + (turned ? c * g.ldo + row : row * g.ldo + c), o[j]);
                             }
                         }
                         continue;
                     }
                     uint32_t w[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) w[j] = pack_out(o[2 * j], o[2 * j + 1], g.mode == kFinish && g.bf16);
-                    if (!(g.mode == kFinish && g.transposed)) {
+                    for (int j = 0; j < 16; ++j) w[j] = pack_out(o[2 * j], o[2 * j + 1], out_bf16);
+                    if (!turned) {
 #pragma unroll
                         for (int p = 0; p < 4; ++p)
                             *piece(first, p) = make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
                     }
-                    if (mirror || (g.mode == kFinish && g.transposed)) {
+                    if (mirror || turned) {
                         // column j of the warp's rows as row j of the second box
                         uint16_t *b = reinterpret_cast<uint16_t *>(second) + 32 * half * 32 + lane;
 #pragma unroll
@@ -548,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
                             b[(2 * j) * 32] = (uint16_t)w[j];
                             b[(2 * j + 1) * 32] = (uint16_t)(w[j] >> 16);
                         }
-                    } else if (g.tail) {
+                    } else if (tail) {
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
                             uint32_t lo[4];
@@ -562,27 +570,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
                         }
                     }
                 }
-                if (g.mode == kFinish && g.O) continue;
+                if (plain) continue;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if (!(g.mode == kFinish && g.transposed)) tma_store_3d(&maps.out, col, row0, z, base + box(k, 0));
-                    if (mirror || (g.mode == kFinish && g.transposed))
+                    if (!turned) tma_store_3d(&maps.out, col, row0, z, base + box(k, 0));
+                    if (mirror || turned)
                         tma_store_3d(&maps.second, row0, col, z, base + box(k, 1));
-                    else if (g.tail) tma_store_3d(&maps.second, col, row0, z, base + box(k, 1));
+                    else if (tail) tma_store_3d(&maps.second, col, row0, z, base + box(k, 1));
                     bulk_commit();
                 }
             }
             // every TMEM read of accumulator a is done: hand it back
             tc5::fence_before();
             __syncwarp();
-            if (lane == 0) tc5::arrive_cluster(cluster::map(acc_empty(a), 0));
+            if (lane == 0) {
+                tc5::arrive_cluster(cluster::map(acc_empty(a), 0));
+                // the stores are complete: count this warp
+                bulk_wait<0>();
+                asm volatile("fence.proxy.async;\n" ::: "memory");
+                asm volatile("red.release.gpu.global.add.u32 [%0], %1;\n" ::"l"(g.done + z), "r"(1u) : "memory");
+            }
         }
         if (lane == 0) {
             bulk_wait<0>();
             // given up: loads of S in flight land before shared memory goes away
-            for (; turns < issued; ++turns)
-                if (!mbar_wait(s_full(quarter, turns & 1), (turns >> 1) & 1)) record_timeout(g.status);
+            for (; loads < issued; ++loads)
+                if (!mbar_wait(s_full(quarter, loads & 1), (loads >> 1) & 1)) record_timeout(g.status);
         }
     }
     tc5::fence_before();
@@ -614,11 +628,11 @@ int norm_blocks(int64_t m, int64_t n) {
 }
 
 // Regions of the workspace, each a multiple of 256 bytes: X twice (a step
-// reads one and writes the other), its tails twice, S, C, the partial sums
-// and rho.
+// reads one and writes the other), its tails twice, S, C, the partial sums,
+// rho and the counters of finished tiles.
 struct Layout {
     int64_t r, c, ldx, lds;
-    size_t x, s, partial, rho;
+    size_t x, s, partial, rho, done;
     Layout(int64_t m, int64_t n, int64_t batch) {
         r = m < n ? m : n;
         c = m < n ? n : m;
@@ -628,8 +642,9 @@ struct Layout {
         s = (size_t)round256(batch * r * lds * 2);
         partial = (size_t)round256(batch * norm_blocks(m, n) * 8);
         rho = (size_t)round256(batch * 4);
+        done = (size_t)round256((batch + 1) * 4);
     }
-    size_t total() const { return 4 * x + 2 * s + partial + rho; }
+    size_t total() const { return 4 * x + 2 * s + partial + rho + done; }
 };
 
 // An f16 (or 16-bit) matrix per batch entry, inner x rows; ld and stride in elements.
@@ -658,52 +673,68 @@ int make_map(CUtensorMap *map, const Matrix &x, int64_t batch, int box_inner, in
     return r == CUDA_SUCCESS ? TRSM_SUCCESS : TRSM_ERR_CUDA_BASE + (int)cudaErrorInvalidValue;
 }
 
-int sm_count(int *out) {
-    static int sms = 0;
-    if (!sms) {
-        int dev = 0, v = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+// CTA pairs that run at once, one CTA an SM.
+int most_pairs(int *out) {
+    static int pairs[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
+    if (e != cudaSuccess) return cuda_status(e);
+    if (!pairs[dev]) {
+        e = cudaFuncSetAttribute(schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         if (e != cudaSuccess) return cuda_status(e);
-        sms = v;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(192);
+        cfg.dynamicSmemBytes = kSmemBytes;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, schedule_kernel, &cfg);
+        if (e != cudaSuccess) return cuda_status(e);
+        if (n < 1) return TRSM_ERR_CUDA_BASE + (int)cudaErrorNotSupported;
+        pairs[dev] = n;
     }
-    *out = sms;
+    *out = pairs[dev];
     return TRSM_SUCCESS;
 }
 
-template <int BN, bool BMN>
-int launch_product(const Maps &maps, const ProductArgs &g, int sms, cudaStream_t st) {
-    using R = Ring<BN>;
-    cudaError_t e = cudaFuncSetAttribute(product_kernel<BN, BMN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)R::kSmem);
-    if (e != cudaSuccess) return cuda_status(e);
-    const int pairs = g.tiles < sms / 2 ? g.tiles : sms / 2;
-    product_kernel<BN, BMN><<<2 * pairs, 192, R::kSmem, st>>>(maps, g);
-    return launch_status();
-}
-
-// The column tile of a product and its tiles, counted into g.
-int plan(ProductArgs &g, int sms, int *bn) {
-    // 256 x 128 tiles while 256 x 256 ones would leave CTA pairs without one
-    const int64_t wide = (int64_t)((g.M + 255) / 256) * ((g.N + 255) / 256) * g.batch;
-    *bn = g.N <= 128 || wide < sms / 2 ? 128 : 256;
-    g.tiles_m = (g.M + kTileM - 1) / kTileM;
-    g.tiles_n = (g.N + *bn - 1) / *bn;
-    int64_t per = (int64_t)g.tiles_m * g.tiles_n;
-    if (g.symmetric) {
-        per = 0;
-        for (int tm = 0; tm < g.tiles_m; ++tm) {
-            const int w = kTileM / *bn * (tm + 1);
-            per += w < g.tiles_n ? w : g.tiles_n;
+// Tiles of r x N products for every matrix (symmetric: N = r, down to the
+// diagonal's): 128 columns wide where that takes less time.  A pair's tile
+// costs its width and about 32 columns' time besides; one matrix's product
+// takes whole rounds of the pairs, those of several run into each other.
+Tiling tiling(int64_t r, int64_t N, bool symmetric, int64_t batch, int pairs) {
+    Tiling best = {};
+    double least = 0;
+    for (int bn = 256; bn >= 128; bn /= 2) {
+        Tiling t = {bn, (int)((r + kTileM - 1) / kTileM), (int)((N + bn - 1) / bn), 0};
+        if (symmetric) {
+            for (int tm = 0; tm < t.tiles_m; ++tm) {
+                const int w = kTileM / bn * (tm + 1);
+                t.per += w < t.tiles_n ? w : t.tiles_n;
+            }
+        } else {
+            t.per = t.tiles_m * t.tiles_n;
+        }
+        double rounds = (double)t.per * batch / pairs;
+        if (batch == 1) rounds = ceil(rounds);
+        if (rounds < 1) rounds = 1;
+        const double cost = rounds * (bn + 32);
+        if (!best.bn || cost < least) {
+            best = t;
+            least = cost;
         }
     }
-    if (per * g.batch > 0x7fffffff) return -11;
-    g.tiles = (int)(per * g.batch);
-    return TRSM_SUCCESS;
+    return best;
 }
 
 template <typename T>
-int convert(const OrthArgs &a, const Input &in, const Halves &x, double *partial, float *rho, cudaStream_t st) {
+int convert(const OrthArgs &a, const Input &in, const Halves &x, double *partial, float *rho, unsigned *done,
+            cudaStream_t st) {
     const int nb = norm_blocks(a.m, a.n);
     norm_kernel<T><<<dim3(nb, (unsigned)a.batch), kNormThreads, 0, st>>>(in, partial);
     int rc = launch_status();
@@ -713,15 +744,15 @@ int convert(const OrthArgs &a, const Input &in, const Halves &x, double *partial
     const dim3 grid((unsigned)(tiles < most ? tiles : most), (unsigned)a.batch);
     void *out = a.steps ? nullptr : a.O;
     if (a.m > a.n)
-        convert_kernel<T, true><<<grid, 256, 0, st>>>(in, partial, nb, a.eps, x, rho, out, a.ldo, a.strideO,
+        convert_kernel<T, true><<<grid, 256, 0, st>>>(in, partial, nb, a.eps, x, rho, done, out, a.ldo, a.strideO,
                                                       a.out_dtype == TRSM_ELEM_BF16);
     else
-        convert_kernel<T, false><<<grid, 256, 0, st>>>(in, partial, nb, a.eps, x, rho, out, a.ldo, a.strideO,
+        convert_kernel<T, false><<<grid, 256, 0, st>>>(in, partial, nb, a.eps, x, rho, done, out, a.ldo, a.strideO,
                                                        a.out_dtype == TRSM_ELEM_BF16);
     return launch_status();
 }
 
-int run(const OrthArgs &a, cudaStream_t st) {
+int run(const OrthArgs &a, unsigned long long tails, cudaStream_t st) {
     const Layout w(a.m, a.n, a.batch);
     char *p = static_cast<char *>(a.ws);
     __half *xh[2], *xl[2];
@@ -732,40 +763,43 @@ int run(const OrthArgs &a, cudaStream_t st) {
     __half *S = reinterpret_cast<__half *>(p + 4 * w.x), *C = reinterpret_cast<__half *>(p + 4 * w.x + w.s);
     double *partial = reinterpret_cast<double *>(p + 4 * w.x + 2 * w.s);
     float *rho = reinterpret_cast<float *>(p + 4 * w.x + 2 * w.s + w.partial);
+    unsigned *done = reinterpret_cast<unsigned *>(p + 4 * w.x + 2 * w.s + w.partial + w.rho);
 
     const int64_t es = a.in_dtype == TRSM_ELEM_F32 ? 4 : 2;
     Input in = {a.G, a.m, a.n, a.ldg, a.strideG, false};
-    uintptr_t bits = (uintptr_t)a.G | (uintptr_t)(a.n * es);
-    if (a.m > 1) bits |= (uintptr_t)(a.ldg * es);
-    if (a.batch > 1) bits |= (uintptr_t)(a.strideG * es);
-    in.vec = bits % 16 == 0;
-    const bool exact = a.in_dtype != TRSM_ELEM_F32;
-    bool tail = has_tail(a.coef, a.steps, 0, exact);
-    const Halves x0 = {xh[0], tail ? xl[0] : nullptr, w.r, w.c, w.ldx, w.r * w.ldx};
-    int rc, sms = 0;
+    in.vec = rows_on_16_bytes(a.G, a.m, a.ldg, a.batch, a.strideG, es);
+    const Halves x0 = {xh[0], tails & 1 ? xl[0] : nullptr, w.r, w.c, w.ldx, w.r * w.ldx};
+    int rc;
     switch (a.in_dtype) {
-        case TRSM_ELEM_F32: rc = convert<float>(a, in, x0, partial, rho, st); break;
-        case TRSM_ELEM_F16: rc = convert<__half>(a, in, x0, partial, rho, st); break;
-        default: rc = convert<__nv_bfloat16>(a, in, x0, partial, rho, st); break;
+        case TRSM_ELEM_F32: rc = convert<float>(a, in, x0, partial, rho, done, st); break;
+        case TRSM_ELEM_F16: rc = convert<__half>(a, in, x0, partial, rho, done, st); break;
+        default: rc = convert<__nv_bfloat16>(a, in, x0, partial, rho, done, st); break;
     }
-    if (!rc) rc = sm_count(&sms);
     if (rc || !a.steps) return rc;
 
-    // The two shapes of product, and every tensor map that the steps use: each
-    // buffer in each part that it plays, by turns for X.
-    ProductArgs sym = {}, app = {};
-    sym.M = sym.N = app.M = (int)w.r;
-    app.N = (int)w.c;
-    app.K = (int)w.r;
-    sym.batch = app.batch = (int)a.batch;
-    sym.symmetric = 1;
-    int bn_sym, bn_app;
-    rc = plan(sym, sms, &bn_sym);
-    if (!rc) rc = plan(app, sms, &bn_app);
-    if (!rc) rc = device_status_word(&sym.status);
-    app.status = sym.status;
+    Schedule g = {};
+    int pairs = 0;
+    rc = most_pairs(&pairs);
+    if (!rc) rc = device_status_word(&g.status);
+    if (rc) return rc;
+    g.r = (int)w.r;
+    g.c = (int)w.c;
+    g.batch = (int)a.batch;
+    g.steps = a.steps;
+    g.sym = tiling(w.r, w.r, true, a.batch, pairs);
+    g.app = tiling(w.r, w.c, false, a.batch, pairs);
+    const int64_t tiles = (2 * (int64_t)g.sym.per + g.app.per) * a.batch * a.steps;
+    if (tiles > 0x0fffffff) return -11;
+    g.tiles = (int)tiles;
+    g.tails = tails;
+    g.rho = rho;
+    g.done = done;
+    for (int i = 0; i < 3 * a.steps; ++i) g.coef[i] = (float)a.coef[i];
+
+    // every tensor map that the steps use: each buffer in each part that it
+    // plays, by turns for X
     const Matrix mS = {S, w.r, w.r, w.lds, w.r * w.lds}, mC = {C, w.r, w.r, w.lds, w.r * w.lds};
-    Maps gram[2], poly, apply[2];
+    Maps *const gram = g.gram, *const apply = g.apply, &poly = g.poly;
     auto map = [&](CUtensorMap *m, const Matrix &x, int inner, int rows, bool swizzled = true) {
         if (!rc) rc = make_map(m, x, a.batch, inner, rows, swizzled);
     };
@@ -774,7 +808,7 @@ int run(const OrthArgs &a, cudaStream_t st) {
         if (k && a.steps == 1) break;
         // S = X X^T
         map(&gram[k].a, mX, kBK, 128);
-        map(&gram[k].b_hi, mX, kBK, bn_sym / 2);
+        map(&gram[k].b_hi, mX, kBK, g.sym.bn / 2);
         gram[k].b_lo = gram[k].b_hi;
         if (k == 0) {
             map(&gram[0].out, mS, 64, 32);
@@ -791,7 +825,7 @@ int run(const OrthArgs &a, cudaStream_t st) {
         map(&apply[k ^ 1].second, mL, 64, 32);
     }
     map(&poly.a, mS, kBK, 128);
-    map(&poly.b_hi, mS, kBK, bn_sym / 2);
+    map(&poly.b_hi, mS, kBK, g.sym.bn / 2);
     poly.b_lo = poly.b_hi;
     map(&poly.out, mC, 64, 32);
     map(&poly.second, mC, 32, 64, false);
@@ -799,12 +833,10 @@ int run(const OrthArgs &a, cudaStream_t st) {
     map(&apply[0].a, mC, kBK, 128);
     apply[1].a = apply[0].a;
     // the last product writes O, by TMA where its rows start on 16-byte boundaries
-    Maps finish = apply[(a.steps - 1) & 1];
+    Maps &finish = g.finish;
+    finish = apply[(a.steps - 1) & 1];
     const bool tall = a.m > a.n;
-    uintptr_t ob = (uintptr_t)a.O;
-    if (a.m > 1) ob |= (uintptr_t)(a.ldo * 2);
-    if (a.batch > 1) ob |= (uintptr_t)(a.strideO * 2);
-    const bool direct = ob % 16 != 0;
+    const bool direct = !rows_on_16_bytes(a.O, a.m, a.ldo, a.batch, a.strideO, 2);
     if (!direct) {
         // strides of a single row or matrix are of no account, but a map needs valid ones
         const int64_t ld = a.m > 1 ? a.ldo : up8(a.n), so = a.batch > 1 ? a.strideO : up8(a.m * ld);
@@ -814,54 +846,40 @@ int run(const OrthArgs &a, cudaStream_t st) {
         else finish.second = finish.out;
     }
 
-    for (int k = 0; k < a.steps && !rc; ++k) {
-        const double ca = a.coef[3 * k], cb = a.coef[3 * k + 1], cc = a.coef[3 * k + 2];
-        const int from = k & 1;
-        const bool last = k + 1 == a.steps;
-        ProductArgs g = sym;
-        g.mode = kGram;
-        g.K = (int)w.c;
-        g.halves = 1;
-        g.rho = k == 0 ? rho : nullptr;
-        g.alpha = kScaleS / (kScaleX * kScaleX);
-        rc = bn_sym == 256 ? launch_product<256, false>(gram[from], g, sms, st)
-                           : launch_product<128, false>(gram[from], g, sms, st);
-        if (rc) break;
-        g.mode = kPoly;
-        g.K = (int)w.r;
-        g.rho = nullptr;
-        g.alpha = (float)cc / kScaleS;
-        g.beta = (float)cb;
-        g.diag = (float)ca * kScaleS;
-        rc = bn_sym == 256 ? launch_product<256, false>(poly, g, sms, st)
-                           : launch_product<128, false>(poly, g, sms, st);
-        if (rc) break;
-        g = app;
-        g.mode = last ? kFinish : kApply;
-        g.halves = tail ? 2 : 1;
-        g.rho = k == 0 ? rho : nullptr;
-        g.alpha = last ? 1.f / (kScaleS * kScaleX) : 1.f / kScaleS;
-        tail = !last && has_tail(a.coef, a.steps, k + 1, exact);
-        g.tail = tail;
-        if (last) {
-            g.transposed = tall;
-            g.bf16 = a.out_dtype == TRSM_ELEM_BF16;
-            g.O = direct ? a.O : nullptr;
-            g.ldo = a.ldo;
-            g.strideO = a.strideO;
-        }
-        const Maps &m = last ? finish : apply[from];
-        rc = bn_app == 256 ? launch_product<256, true>(m, g, sms, st) : launch_product<128, true>(m, g, sms, st);
-    }
-    return rc;
+    if (rc) return rc;
+    g.transposed = tall;
+    g.bf16 = a.out_dtype == TRSM_ELEM_BF16;
+    g.O = direct ? a.O : nullptr;
+    g.ldo = a.ldo;
+    g.strideO = a.strideO;
+
+    const int64_t first = (int64_t)(g.sym.per > g.app.per ? g.sym.per : g.app.per) * a.batch;  // tiles at one time
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)(first < pairs ? first : pairs));
+    cfg.blockDim = dim3(192);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeCooperative;  // all pairs run at once
+    at[0].val.cooperative = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, schedule_kernel, g));
 }
 
 }  // namespace orth
 
-size_t orth_workspace_bytes(int, int64_t m, int64_t n, int64_t batch, int64_t) {
+size_t orth_workspace_bytes(int, int64_t m, int64_t n, int64_t batch, int64_t steps) {
+    if (orth_small_usable(m, n, steps)) return 0;
     return orth::Layout(m, n, batch).total();
 }
 
-int orth_run(const OrthArgs &a, cudaStream_t st) { return orth::run(a, st); }
+int orth_run(const OrthArgs &a, cudaStream_t st) {
+    unsigned long long tails = 0;
+    for (int k = 0; k < a.steps; ++k)
+        if (orth::has_tail(a.coef, a.steps, k, a.in_dtype != TRSM_ELEM_F32)) tails |= 1ull << k;
+    if (orth_small_usable(a.m, a.n, a.steps)) return orth_small(a, tails, st);
+    return orth::run(a, tails, st);
+}
 
 }  // namespace trsm

@@ -1,0 +1,130 @@
+// What the orthogonalisation's paths share: the input, its norm and scale,
+// and the split of a value into an f16 head and tail.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace trsm {
+namespace orth {
+
+constexpr float kScaleX = 16384.f, kScaleS = 4096.f;  // 2^14, 2^12
+
+// ------------------------------------------------------------------ |G|_F and the f16 copy
+template <typename T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// Sum of squares without overflow or underflow (J. L. Blue, "A portable
+// Fortran program to find the Euclidean norm of a vector", ACM TOMS 4(1),
+// 1978): large and small values are squared scaled, each kind on its own.
+struct Squares {
+    float big = 0.f, mid = 0.f, small = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float y = fabsf(x);
+        if (y > 0x1p48f || y < 0x1p-48f) {
+            const float b = x * 0x1p-75f, s = x * 0x1p75f;
+            if (y > 1.f) big = fmaf(b, b, big);
+            else small = fmaf(s, s, small);
+        } else {
+            mid = fmaf(x, x, mid);  // NaN too
+        }
+    }
+    // Eight at once: plainly where their sum shows that none overflowed and
+    // what underflowed does not count.
+    __device__ __forceinline__ void add_8(const float (&v)[8]) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s = fmaf(v[k], v[k], s);
+        if (s > 0x1p-80f && s < 0x1p100f) {
+            mid += s;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) add(v[k]);
+        }
+    }
+    __device__ __forceinline__ double total() const {
+        return (double)big * 0x1p150 + (double)mid + (double)small * 0x1p-150;
+    }
+};
+
+// Sum over a block's threads, in a fixed order; valid in thread 0.
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double part[32];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_down_sync(~0u, v, o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int w = 1; w < (int)blockDim.x / 32; ++w) v += part[w];
+    return v;
+}
+
+struct Input {
+    const void *G;
+    int64_t m, n, ld, stride;  // rows, columns as given
+    bool vec;                  // every row starts on a 16-byte boundary
+};
+inline bool rows_on_16_bytes(const void *p, int64_t m, int64_t ld, int64_t batch, int64_t stride, int64_t elem) {
+    uintptr_t bits = (uintptr_t)p;
+    if (m > 1) bits |= (uintptr_t)(ld * elem);
+    if (batch > 1) bits |= (uintptr_t)(stride * elem);
+    return bits % 16 == 0;
+}
+
+constexpr int kMaxSteps = 64;
+
+// 1 / (|G|_F + eps) as 2^e rho, rho in [1, 2); NaN where it is no positive
+// number.
+struct Scale {
+    float up, more, rho;  // 2^e = up * more, neither of which overflows
+};
+__device__ __forceinline__ Scale scale_from(double sum_of_squares, double eps) {
+    const double s = 1.0 / (sqrt(sum_of_squares) + eps);
+    if (!(s > 0 && s < 1e300)) return {1.f, 1.f, __int_as_float(0x7fffffff)};
+    int e = ilogb(s);
+    const float rho = (float)scalbn(s, -e);
+    e = min(max(e, -160), 240);
+    return {scalbnf(1.f, e / 2), scalbnf(1.f, e - e / 2), rho};
+}
+// The same from a matrix's partial sums, by a whole block; every thread gets
+// the same.
+__device__ __forceinline__ Scale scale_of(const double *partial, int count, double eps) {
+    __shared__ Scale shared;
+    if (threadIdx.x < 32) {
+        double sum = 0;
+        for (int i = threadIdx.x; i < count; i += 32) sum += partial[i];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_down_sync(~0u, sum, o);
+        if (threadIdx.x == 0) shared = scale_from(sum, eps);
+    }
+    __syncthreads();
+    return shared;
+}
+
+__device__ __forceinline__ void split(float x, __half &hi, __half &lo) {
+    hi = __float2half_rn(x);
+    lo = __float2half_rn(x - __half2float(hi));
+}
+
+// Eight elements of a row of G from column j on, zero past column n.
+template <typename T>
+__device__ __forceinline__ void load_8(const T *row, int64_t j, int64_t n, bool vec, float (&g)[8]) {
+    if (vec && j + 8 <= n) {
+        alignas(16) T v[8];
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+            reinterpret_cast<uint4 *>(v)[k] = reinterpret_cast<const uint4 *>(row + j)[k];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[k] = to_f32<T>(v[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[k] = j + k < n ? to_f32<T>(row[j + k]) : 0.f;
+    }
+}
+
+}  // namespace orth
+}  // namespace trsm

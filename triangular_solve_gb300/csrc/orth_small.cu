@@ -1,0 +1,347 @@
+// Newton-Schulz orthogonalisation of small matrices: one CTA takes one matrix
+// from the norm to the result, with X (head and tail), S and C in shared
+// memory throughout.
+//
+// A matrix of at most 128 rows (after transposition) is far too small for a
+// 256-row tensor-core tile, and its fifteen dependent products are bound by
+// the way from one to the next, not by their arithmetic.  So the products
+// are warp-level matrix instructions (m16n8k16, f16 factors, f32 sums) whose
+// operands come straight from shared memory: a product costs a barrier
+// instead of a launch and two trips through L2.
+#include <math.h>
+#include <stdint.h>
+
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "mbarrier.cuh"
+#include "orth.h"
+#include "orth_convert.cuh"
+#include "trsm_model.h"
+
+namespace trsm {
+namespace orth {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+
+struct SmallArgs {
+    Input in;
+    int r, c, cp, ldx;  // c rounded up to 16; row length of X in shared memory
+    int tall, steps, any_tail;
+    unsigned long long tails;  // bit k: X_k has a tail
+    double eps;
+    void *O;
+    int64_t ldo, strideO;
+    int bf16, vec;  // of O
+    float coef[3 * kMaxSteps];
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&v)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&v)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Tiles of the R x R products: WM x WN for each warp, the K dimension of
+// X X^T cut between the warps where there are fewer tiles than warps.
+template <int R> struct SmallShape {
+    static constexpr int WM = R == 128 ? 32 : 16, WN = R == 128 ? 64 : 32;
+    static constexpr int kTiles = (R / WM) * (R / WN), kCut = kWarps / kTiles;
+    static constexpr int ld = R + 8;  // of S and C: rows 16 bytes apart in the banks
+    static constexpr size_t kScratch = kCut > 1 ? (size_t)kWarps * WM * WN * 4 : 0;
+    static size_t smem(int ldx, bool tail) {
+        return (size_t)R * ldx * 2 * (tail ? 2 : 1) + 2 * (size_t)R * ld * 2 + kScratch;
+    }
+};
+
+// acc += A[m0 ..][k0 ..] B[n0 ..][k0 ..]^T over `kn` steps of 16, both in
+// shared memory with rows along K.
+template <int WM, int WN>
+__device__ __forceinline__ void tile_product(float (&acc)[WM / 16][WN / 8][4], uint32_t A, int lda, int m0, uint32_t B,
+                                             int ldb, int n0, int k0, int kn) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t pa = A + 2 * ((m0 + (lane & 15)) * lda + k0 + (lane >> 4) * 8);
+    const uint32_t pb = B + 2 * ((n0 + (lane & 7) + (lane >> 4) * 8) * ldb + k0 + ((lane >> 3) & 1) * 8);
+#pragma unroll 2
+    for (int k = 0; k < kn; ++k) {
+        uint32_t a[WM / 16][4], b[WN / 16][4];
+#pragma unroll
+        for (int i = 0; i < WM / 16; ++i) ldmatrix4(a[i], pa + 2 * (16 * i * lda + 16 * k));
+#pragma unroll
+        for (int j = 0; j < WN / 16; ++j) ldmatrix4(b[j], pb + 2 * (16 * j * ldb + 16 * k));
+#pragma unroll
+        for (int i = 0; i < WM / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < WN / 8; ++j) mma_f16(acc[i][j], a[i], b[j / 2][2 * (j & 1)], b[j / 2][2 * (j & 1) + 1]);
+    }
+}
+
+template <typename T, int R>
+__global__ void __launch_bounds__(kThreads) small_kernel(const __grid_constant__ SmallArgs g) {
+    using W = SmallShape<R>;
+    constexpr int WM = W::WM, WN = W::WN;
+    extern __shared__ __align__(16) unsigned char small_smem[];
+    __half *const Xh = reinterpret_cast<__half *>(small_smem);
+    __half *const Xl = Xh + (size_t)R * g.ldx;
+    __half *const S = Xh + (size_t)R * g.ldx * (g.any_tail ? 2 : 1), *const C = S + R * W::ld;
+    float *const scratch = reinterpret_cast<float *>(C + R * W::ld);
+    __shared__ Scale scale;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t z = blockIdx.x;
+    const T *G = static_cast<const T *>(g.in.G) + z * g.in.stride;
+    const int m = (int)g.in.m, n = (int)g.in.n, per = (n + 7) / 8;
+
+    // |G|_F, while X is set to zero (its padding stays so)
+    Squares sq;
+    for (int e = tid; e < m * per; e += kThreads) {
+        float v[8];
+        load_8<T>(G + (int64_t)(e / per) * g.in.ld, e % per * 8, n, g.in.vec, v);
+        sq.add_8(v);
+    }
+    for (int e = tid; e < R * g.ldx * (g.any_tail ? 2 : 1) / 8; e += kThreads)
+        reinterpret_cast<uint4 *>(Xh)[e] = make_uint4(0, 0, 0, 0);
+    const double sum = block_sum(sq.total());
+    if (tid == 0) scale = scale_from(sum, g.eps);
+    __syncthreads();
+    const float rho = scale.rho;
+
+    // X_0
+    for (int e = tid; e < m * per; e += kThreads) {
+        const int i = e / per, j = e % per * 8;
+        float v[8];
+        load_8<T>(G + (int64_t)i * g.in.ld, j, n, g.in.vec, v);
+        alignas(16) __half hi[8], lo[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) split(v[k] * scale.up * scale.more * kScaleX, hi[k], lo[k]);
+        if (!g.tall) {
+            *reinterpret_cast<uint4 *>(Xh + i * g.ldx + j) = *reinterpret_cast<const uint4 *>(hi);
+            if (g.tails & 1) *reinterpret_cast<uint4 *>(Xl + i * g.ldx + j) = *reinterpret_cast<const uint4 *>(lo);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (j + k < n) {
+                    Xh[(j + k) * g.ldx + i] = hi[k];
+                    if (g.tails & 1) Xl[(j + k) * g.ldx + i] = lo[k];
+                }
+            }
+        }
+    }
+    __syncthreads();
+
+    const uint32_t xh = smem_u32(Xh), xl = smem_u32(Xl), sS = smem_u32(S), sC = smem_u32(C);
+    const int tile = warp % W::kTiles, cut = warp / W::kTiles;
+    const int m0 = tile / (R / WN) * WM, n0 = tile % (R / WN) * WN;
+    const int row = lane >> 2, col = (lane & 3) * 2;  // of a fragment's first pair; the second is 8 rows on
+    for (int s = 0; s < g.steps; ++s) {
+        const bool split_x = (g.tails >> s) & 1, split_next = (g.tails >> (s + 1)) & 1, last = s + 1 == g.steps;
+        {  // S = X X^T
+            float acc[WM / 16][WN / 8][4] = {};
+            const int all = g.cp / 16, each = (all + W::kCut - 1) / W::kCut;
+            const int k0 = cut * each, k1 = k0 + each < all ? k0 + each : all;
+            if (k0 < k1) tile_product<WM, WN>(acc, xh, g.ldx, m0, xh, g.ldx, n0, 16 * k0, k1 - k0);
+            const float alpha = kScaleS / (kScaleX * kScaleX) * (s == 0 ? rho * rho : 1.f);
+            if constexpr (W::kCut == 1) {
+#pragma unroll
+                for (int i = 0; i < WM / 16; ++i)
+#pragma unroll
+                    for (int j = 0; j < WN / 8; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            *reinterpret_cast<__half2 *>(S + (m0 + 16 * i + row + 8 * h) * W::ld + n0 + 8 * j + col) =
+                                __floats2half2_rn(alpha * acc[i][j][2 * h], alpha * acc[i][j][2 * h + 1]);
+            } else {
+                float *mine = scratch + warp * (WM * WN);
+#pragma unroll
+                for (int i = 0; i < WM / 16; ++i)
+#pragma unroll
+                    for (int j = 0; j < WN / 8; ++j)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) mine[((i * (WN / 8) + j) * 4 + q) * 32 + lane] = acc[i][j][q];
+                __syncthreads();
+                // the first cut's warps add the others', in order
+                if (cut == 0) {
+#pragma unroll
+                    for (int i = 0; i < WM / 16; ++i)
+#pragma unroll
+                        for (int j = 0; j < WN / 8; ++j) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                for (int p = 1; p < W::kCut; ++p)
+                                    acc[i][j][q] += scratch[(p * W::kTiles + tile) * (WM * WN) +
+                                                            ((i * (WN / 8) + j) * 4 + q) * 32 + lane];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                *reinterpret_cast<__half2 *>(S + (m0 + 16 * i + row + 8 * h) * W::ld + n0 + 8 * j + col) =
+                                    __floats2half2_rn(alpha * acc[i][j][2 * h], alpha * acc[i][j][2 * h + 1]);
+                        }
+                }
+            }
+        }
+        __syncthreads();
+        if (cut == 0) {  // C = a I + b S + c S^2
+            float acc[WM / 16][WN / 8][4] = {};
+            tile_product<WM, WN>(acc, sS, W::ld, m0, sS, W::ld, n0, 0, R / 16);
+            const float diag = g.coef[3 * s] * kScaleS, beta = g.coef[3 * s + 1], alpha = g.coef[3 * s + 2] / kScaleS;
+#pragma unroll
+            for (int i = 0; i < WM / 16; ++i)
+#pragma unroll
+                for (int j = 0; j < WN / 8; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int y = m0 + 16 * i + row + 8 * h, x = n0 + 8 * j + col;
+                        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(S + y * W::ld + x));
+                        const float o0 = fmaf(beta, b.x, alpha * acc[i][j][2 * h]) + (x == y ? diag : 0.f);
+                        const float o1 = fmaf(beta, b.y, alpha * acc[i][j][2 * h + 1]) + (x + 1 == y ? diag : 0.f);
+                        *reinterpret_cast<__half2 *>(C + y * W::ld + x) = __floats2half2_rn(o0, o1);
+                    }
+        }
+        __syncthreads();
+        // X = C X in place: a warp holds 16 columns of X in registers and
+        // writes them anew row tile by row tile
+        float alpha = (s == 0 ? rho : 1.f) / kScaleS;
+        if (last) alpha /= kScaleX;
+        for (int j0 = 16 * warp; j0 < g.cp; j0 += 16 * kWarps) {
+            uint32_t bh[R / 16][4], bl[R / 16][4];
+            const uint32_t at = 2 * ((lane & 15) * g.ldx + j0 + (lane >> 4) * 8);
+#pragma unroll
+            for (int k = 0; k < R / 16; ++k) ldmatrix4_trans(bh[k], xh + at + 2 * 16 * k * g.ldx);
+            if (split_x) {
+#pragma unroll
+                for (int k = 0; k < R / 16; ++k) ldmatrix4_trans(bl[k], xl + at + 2 * 16 * k * g.ldx);
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int i = 0; i < R / 16; ++i) {
+                float acc[2][4] = {};
+                const uint32_t pa = sC + 2 * ((16 * i + (lane & 15)) * W::ld + (lane >> 4) * 8);
+#pragma unroll
+                for (int k = 0; k < R / 16; ++k) {
+                    uint32_t a[4];
+                    ldmatrix4(a, pa + 2 * 16 * k);
+                    mma_f16(acc[0], a, bh[k][0], bh[k][1]);
+                    mma_f16(acc[1], a, bh[k][2], bh[k][3]);
+                    if (split_x) {
+                        mma_f16(acc[0], a, bl[k][0], bl[k][1]);
+                        mma_f16(acc[1], a, bl[k][2], bl[k][3]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int p = (16 * i + row + 8 * h) * g.ldx + j0 + 8 * j + col;
+                        const float o0 = alpha * acc[j][2 * h], o1 = alpha * acc[j][2 * h + 1];
+                        if (last && g.bf16) {  // the result's bits, in X's place
+                            *reinterpret_cast<__nv_bfloat162 *>(Xh + p) = __floats2bfloat162_rn(o0, o1);
+                        } else {
+                            const __half2 hi = __floats2half2_rn(o0, o1);
+                            *reinterpret_cast<__half2 *>(Xh + p) = hi;
+                            if (split_next)
+                                *reinterpret_cast<__half2 *>(Xl + p) =
+                                    __floats2half2_rn(o0 - __low2float(hi), o1 - __high2float(hi));
+                        }
+                    }
+            }
+        }
+        __syncthreads();
+    }
+
+    uint16_t *O = static_cast<uint16_t *>(g.O) + z * g.strideO;
+    const uint16_t *X = reinterpret_cast<const uint16_t *>(Xh);
+    if (!g.tall && g.vec) {
+        for (int e = tid; e < m * per; e += kThreads) {
+            const int i = e / per, j = e % per * 8;
+            if (j + 8 <= n) {
+                *reinterpret_cast<uint4 *>(O + i * g.ldo + j) = *reinterpret_cast<const uint4 *>(X + i * g.ldx + j);
+            } else {
+                for (int k = j; k < n; ++k) O[i * g.ldo + k] = X[i * g.ldx + k];
+            }
+        }
+    } else {
+        for (int e = tid; e < m * n; e += kThreads) {
+            const int i = e / n, j = e % n;
+            O[i * g.ldo + j] = g.tall ? X[j * g.ldx + i] : X[i * g.ldx + j];
+        }
+    }
+}
+
+// ------------------------------------------------------------------ launch
+constexpr size_t kMostSmem = 224 * 1024;
+
+// With a tail, which the coefficients may ask for or not: whether a call
+// needs a workspace depends on the shape alone.
+template <int R> bool fits(int64_t c) {
+    return SmallShape<R>::smem((int)((c + 15) / 16 * 16 + 8), true) <= kMostSmem;
+}
+// Rows of the kernel that takes r x c matrices, or 0.
+int small_rows(int64_t r, int64_t c) {
+    if (c > 4096) return 0;
+    if (r <= 32) return fits<32>(c) ? 32 : 0;
+    if (r <= 64) return fits<64>(c) ? 64 : 0;
+    if (r <= 128) return fits<128>(c) ? 128 : 0;
+    return 0;
+}
+
+template <typename T, int R> int launch(const SmallArgs &g, int64_t batch, cudaStream_t st) {
+    const size_t smem = SmallShape<R>::smem(g.ldx, g.any_tail);
+    const cudaError_t e = cudaFuncSetAttribute(small_kernel<T, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)kMostSmem);
+    if (e != cudaSuccess) return cuda_status(e);
+    small_kernel<T, R><<<(unsigned)batch, kThreads, smem, st>>>(g);
+    return launch_status();
+}
+template <typename T> int launch_rows(const SmallArgs &g, int rows, int64_t batch, cudaStream_t st) {
+    return rows == 32 ? launch<T, 32>(g, batch, st) : rows == 64 ? launch<T, 64>(g, batch, st)
+                                                                 : launch<T, 128>(g, batch, st);
+}
+
+}  // namespace orth
+
+bool orth_small_usable(int64_t m, int64_t n, int64_t steps) {
+    const int64_t r = m < n ? m : n, c = m < n ? n : m;
+    return steps > 0 && steps < orth::kMaxSteps && orth::small_rows(r, c) > 0;
+}
+
+int orth_small(const OrthArgs &a, unsigned long long tails, cudaStream_t st) {
+    orth::SmallArgs g = {};
+    const int64_t es = a.in_dtype == TRSM_ELEM_F32 ? 4 : 2;
+    g.in = {a.G, a.m, a.n, a.ldg, a.strideG, orth::rows_on_16_bytes(a.G, a.m, a.ldg, a.batch, a.strideG, es)};
+    g.r = (int)(a.m < a.n ? a.m : a.n);
+    g.c = (int)(a.m < a.n ? a.n : a.m);
+    g.cp = (g.c + 15) / 16 * 16;
+    g.ldx = g.cp + 8;
+    g.tall = a.m > a.n;
+    g.steps = a.steps;
+    g.tails = tails;
+    g.any_tail = tails != 0;
+    g.eps = a.eps;
+    g.O = a.O;
+    g.ldo = a.ldo;
+    g.strideO = a.strideO;
+    g.bf16 = a.out_dtype == TRSM_ELEM_BF16;
+    g.vec = orth::rows_on_16_bytes(a.O, a.m, a.ldo, a.batch, a.strideO, 2);
+    for (int i = 0; i < 3 * a.steps; ++i) g.coef[i] = (float)a.coef[i];
+    const int rows = orth::small_rows(g.r, g.c);
+    switch (a.in_dtype) {
+        case TRSM_ELEM_F32: return orth::launch_rows<float>(g, rows, a.batch, st);
+        case TRSM_ELEM_F16: return orth::launch_rows<__half>(g, rows, a.batch, st);
+        default: return orth::launch_rows<__nv_bfloat16>(g, rows, a.batch, st);
+    }
+}
+
+}  // namespace trsm
