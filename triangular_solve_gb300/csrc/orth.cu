@@ -4,7 +4,9 @@
 //
 // for r x c matrices X with r <= c (a taller matrix is taken transposed).
 // Of the three products of a step the first two are symmetric and are
-// computed for their lower tiles only, each stored twice.
+// computed and stored on and below the diagonal only, in tiles of 256 rows;
+// where a product needs what lies above, it reads the tile below it as the
+// transposed operand.
 //
 // Precision.  Every product takes f16 factors and sums in f32.  What the
 // steps amplify is rounding of X in directions where X is small: a step
@@ -167,11 +169,13 @@ __global__ void __launch_bounds__(256) convert_kernel(const Input in, const doub
 // ------------------------------------------------------------------ products
 enum Kind { kGram, kPoly, kApply };  // S = X X^T, C = a I + b S + c S^2, X = C X
 
-// out: the output in boxes of 32 rows x 64 columns (128-byte swizzle).
-// second: kApply the tail's likewise; symmetric or transposed, the output in
-// boxes of 64 rows x 32 columns.  in: kPoly, S as `out`.
+// Operands in slabs of 64 along K: a and b (b_lo: the tail's) K-major, 64 x 128
+// and 64 x bn / 2, but X in C X as 64 x 64 with its columns contiguous, and
+// so `above`, S or C from below the diagonal.
+// out, tail: the output in boxes of 32 rows x 64 columns, but a transposed
+// result in boxes of 64 rows x 32 columns.  in: kPoly, S in boxes like out.
 struct Maps {
-    CUtensorMap a, b_hi, b_lo, out, second, in;
+    CUtensorMap a, above, b, b_lo, out, tail, in;
 };
 
 // Tiles of one kind of product: bn columns wide (128 or 256), per of them a
@@ -198,17 +202,20 @@ struct Schedule {
 
 constexpr int kTileM = 256, kBK = 64;
 constexpr uint32_t kABytes = 128 * kBK * 2;  // 128 rows of A per CTA
+constexpr uint32_t kHalfBytes = 64 * kBK * 2;  // a box of 64 x 64
 constexpr uint32_t kStageBytes = 2 * kABytes;
 constexpr int kStages = 5;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kBox = 32 * 64 * 2;       // bytes of a box of the output
-constexpr uint32_t kOutAt = kStages * kStageBytes;  // output boxes: 2 by turns x 2 for each of 4 warps
-constexpr uint32_t kBarsAt = kOutAt + 16 * kBox;
-constexpr uint32_t kTmemAt = kBarsAt + 8u * (2 * kStages + 5 + 8);
-constexpr size_t kSmemBytes = 1024 + kBarsAt + 256;
-static_assert(kTmemAt + 4 <= kBarsAt + 256 && kSmemBytes <= 227 * 1024, "shared memory");
+constexpr int kOutWarps = 8;                 // that empty the accumulators
+constexpr uint32_t kOutAt = kStages * kStageBytes;  // two output boxes for each of them
+constexpr uint32_t kBarsAt = kOutAt + 2 * kOutWarps * kBox;
+constexpr uint32_t kTmemAt = kBarsAt + 8u * (2 * kStages + 5 + 2 * kOutWarps);
+constexpr int kProductThreads = 32 * (2 + kOutWarps);
+constexpr size_t kSmemBytes = 1024 + kBarsAt + 512;
+static_assert(kTmemAt + 4 <= kBarsAt + 512 && kSmemBytes <= 227 * 1024, "shared memory");
 constexpr int kPatience = 4;                 // full waits for what itself waits for another product
-constexpr unsigned kWarpsATile = 8;          // that store it: four in each CTA
+constexpr unsigned kWarpsATile = 2 * kOutWarps;  // that store it, of both CTAs
 
 __device__ __forceinline__ uint32_t pack_half(float x, float y) {
     const __half2 h = __floats2half2_rn(x, y);
@@ -283,10 +290,9 @@ __device__ __forceinline__ bool wait_done(const Schedule &g, int z, unsigned nee
 // The whole call in one persistent kernel on CTA pairs, one CTA an SM; each
 // pair takes 256 x bn tiles of the schedule in turn.  Warp 0 loads (TMA, a
 // ring of slabs of K = 64), warp 1 of the even CTA issues the MMAs, warps
-// 2..5 empty the accumulators (two in TMEM, so a tile's way out runs under
+// 2..9 empty the accumulators (two in TMEM, so a tile's way out runs under
 // the next one's MMAs): 64 columns at a time through shared memory, from
-// where TMA stores them, rows whole, and for a symmetric product below the
-// diagonal once more transposed.
+// where TMA stores them.
 //
 // A product waits for the one before it matrix by matrix: the warps that
 // store a tile count themselves in done[z] once their stores are complete,
@@ -295,9 +301,10 @@ __device__ __forceinline__ bool wait_done(const Schedule &g, int z, unsigned nee
 // takes its tiles, and the launch is cooperative, so the waits end; they are
 // bounded all the same.
 //
-// B is Y^T for a K-major Y (kGram, kPoly; Y = A's matrix) or a K x N matrix
-// with contiguous N (kApply).
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
+// S = X X^T and S S take both operands along their rows; C X takes X's columns
+// as they lie (MN-major), and what S and C lack above the diagonal is taken
+// from below it in the same way.
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     schedule_kernel(const __grid_constant__ Schedule g) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -317,10 +324,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     const uint32_t rank = cluster::rank();
     const bool leader = rank == 0;
     const int pair = (int)blockIdx.x >> 1, npairs = (int)gridDim.x >> 1;
-    // slabs of a tile: of the head, and in all
-    auto slabs_of = [&](const Tile &x, int &heads) {
-        heads = ((x.kind == kGram ? g.c : g.r) + kBK - 1) / kBK;
-        return x.kind == kApply && ((g.tails >> x.step) & 1) ? 2 * heads : heads;
+    // The slabs of a tile: `heads` with X's head, as many again with its tail;
+    // of each kind, those from `a_above` (`b_above`) on take their part of A
+    // (B) from below the diagonal, or, C X's B, all as columns.
+    struct Slabs {
+        int heads, passes, a_above, b_above;
+    };
+    auto slabs_of = [&](const Tile &x, int bn) {
+        Slabs s;
+        s.heads = ((x.kind == kGram ? g.c : g.r) + kBK - 1) / kBK;
+        s.passes = x.kind == kApply && ((g.tails >> x.step) & 1) ? 2 : 1;
+        s.a_above = x.kind == kGram ? s.heads : min(s.heads, (x.tm + 1) * (kTileM / kBK));
+        s.b_above = x.kind == kGram ? s.heads
+                    : x.kind == kApply ? 0
+                                       : min(s.heads, (x.tn * bn / kTileM + 1) * (kTileM / kBK));
+        return s;
     };
 
     if (threadIdx.x == 0) {
@@ -331,10 +349,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(acc_full(a), 1);
-            mbar_init(acc_empty(a), 8);  // four warps in each CTA
+            mbar_init(acc_empty(a), kWarpsATile);
         }
         mbar_init(drain, 1);
-        for (int w = 0; w < 4; ++w)
+        for (int w = 0; w < kOutWarps; ++w)
             for (int k = 0; k < 2; ++k) mbar_init(s_full(w, k), 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -353,7 +371,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
 
     if (warp == 0) {
         if (lane == 0) {
-            int it = 0;
+            const uint32_t full0 = cluster::map(full(0), 0);
+            int s = 0, filled = 0;  // the next stage; stages in use the first time round
+            uint32_t phase = 1;     // of empty(s), after the first round
             for (int t = pair; t < g.tiles && !aborted(); t += npairs) {
                 const Tile x = tile_at(g, t);
                 const Maps &m = maps_of(g, x);
@@ -361,44 +381,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
                     fail();
                     break;
                 }
-                const bool bmn = x.kind == kApply;
-                const int bn = bmn ? g.app.bn : g.sym.bn;
+                const int bn = x.kind == kApply ? g.app.bn : g.sym.bn;
                 const int ya = x.tm * kTileM + 128 * (int)rank, yb = x.tn * bn + bn / 2 * (int)rank;
-                int heads;
-                const int slabs = slabs_of(x, heads);
-                for (int kb = 0; kb < slabs; ++kb, ++it) {
-                    const int s = it % kStages;
-                    if (it >= kStages && !mbar_wait(empty(s), ((it / kStages) - 1) & 1)) {
-                        fail();
-                        break;
+                const Slabs n = slabs_of(x, bn);
+                const uint32_t bytes = 2 * (kABytes + bn / 2 * kBK * 2);
+                bool ok = true;
+                for (int pass = 0; pass < n.passes && ok; ++pass) {
+                    const CUtensorMap *const columns = x.kind == kPoly ? &m.above : pass ? &m.b_lo : &m.b;
+                    for (int kb = 0; kb < n.heads; ++kb) {
+                        if (filled == kStages) {
+                            if (!mbar_wait(empty(s), phase)) {
+                                ok = false;
+                                break;
+                            }
+                        } else {
+                            ++filled;
+                        }
+                        if (leader) mbar_expect_tx(full(s), bytes);
+                        const uint32_t st = base + s * kStageBytes, fb = full0 + 8 * s;
+                        const int kx = kb * kBK;
+                        if (kb < n.a_above) {
+                            tc5::load_pair(st, &m.a, kx, ya, x.z, fb);
+                        } else {
+                            tc5::load_pair(st, &m.above, ya, kx, x.z, fb);
+                            tc5::load_pair(st + kHalfBytes, &m.above, ya + 64, kx, x.z, fb);
+                        }
+                        if (kb < n.b_above) {
+                            tc5::load_pair(st + kABytes, &m.b, kx, yb, x.z, fb);
+                        } else {
+                            tc5::load_pair(st + kABytes, columns, yb, kx, x.z, fb);
+                            if (bn == 256) tc5::load_pair(st + kABytes + kHalfBytes, columns, yb + 64, kx, x.z, fb);
+                        }
+                        if (++s == kStages) {
+                            s = 0;
+                            phase ^= 1;
+                        }
                     }
-                    if (leader) mbar_expect_tx(full(s), 2 * (kABytes + bn / 2 * kBK * 2));
-                    const uint32_t st = base + s * kStageBytes, fb = cluster::map(full(s), 0);
-                    const int kx = (kb < heads ? kb : kb - heads) * kBK;
-                    const CUtensorMap *mb = kb < heads ? &m.b_hi : &m.b_lo;
-                    tc5::load_pair(st, &m.a, kx, ya, x.z, fb);
-                    if (bmn) {
-                        for (int q = 0; q < bn / 128; ++q)
-                            tc5::load_pair(st + kABytes + q * (64 * kBK * 2), mb, yb + 64 * q, kx, x.z, fb);
-                    } else {
-                        tc5::load_pair(st + kABytes, mb, kx, yb, x.z, fb);
-                    }
+                }
+                if (!ok) {
+                    fail();
+                    break;
                 }
             }
             if (aborted() && leader) {
-                // the pair's loads counted on these barriers land before shared memory goes away
-                for (int j = (it > kStages ? it - kStages : 0); j < it; ++j)
-                    if (!mbar_wait(full(j % kStages), (j / kStages) & 1)) record_timeout(g.status);
+                // the pair's loads counted on these barriers land before shared
+                // memory goes away: the newest of each stage in use
+                for (int j = 0; j < filled; ++j) {
+                    s = s ? s - 1 : kStages - 1;
+                    if (s == kStages - 1) phase ^= 1;
+                    if (!mbar_wait(full(s), phase ^ 1)) record_timeout(g.status);
+                }
             }
         }
     } else if (warp == 1) {
         if (lane == 0 && leader) {
-            int it = 0, i = 0;
+            int i = 0, s = 0;
+            uint32_t phase = 0;  // of full(s)
             for (int t = pair; t < g.tiles && !aborted(); t += npairs, ++i) {
                 const Tile x = tile_at(g, t);
-                const bool bmn = x.kind == kApply;
-                const uint32_t idesc = tc5::idesc_f16(kTileM, bmn ? g.app.bn : g.sym.bn, bmn);
-                const int a = i & 1;
+                const int bn = x.kind == kApply ? g.app.bn : g.sym.bn, a = i & 1;
+                const Slabs n = slabs_of(x, bn);
                 if (i >= 2 && !mbar_wait(acc_empty(a), ((i >> 1) - 1) & 1)) {
                     fail();
                     break;
@@ -406,29 +448,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
                 tc5::fence_after();
                 const uint32_t d = tmem + (uint32_t)(a * 256);
                 bool ok = true;
-                int heads;
-                const int slabs = slabs_of(x, heads);
-                for (int kb = 0; kb < slabs; ++kb, ++it) {
-                    const int s = it % kStages;
-                    // the loader may itself be waiting for an earlier product
-                    bool come = false;
-                    for (int tries = 0; tries < kPatience && !come && !aborted(); ++tries)
-                        come = mbar_wait(full(s), (it / kStages) & 1);
-                    if (!come) {
-                        fail();
-                        ok = false;
-                        break;
-                    }
-                    tc5::fence_after();
-                    const uint32_t st = base + s * kStageBytes;
+                uint32_t accumulate = 0;
+                // slabs kb .. end - 1, all with their operands the same way round
+                auto run = [&](int kb, int end, bool a_mn, bool b_mn) {
+                    // 16 of K are 32 bytes on in a row, 16 rows of 128 bytes otherwise
+                    const uint64_t da0 = a_mn ? tc5::desc_mn_major(base, kHalfBytes) : tc5::desc_k_major(base);
+                    const uint64_t db0 =
+                        b_mn ? tc5::desc_mn_major(base + kABytes, kHalfBytes) : tc5::desc_k_major(base + kABytes);
+                    const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
+                    const uint32_t idesc = tc5::idesc_f16(kTileM, bn, a_mn, b_mn);
+                    for (; kb < end && ok; ++kb) {
+                        bool come = mbar_wait(full(s), phase);
+                        // the loader may itself be waiting for an earlier product
+                        for (int tries = 1; tries < kPatience && !come && !aborted(); ++tries)
+                            come = mbar_wait(full(s), phase);
+                        if (!come) {
+                            fail();
+                            ok = false;
+                            break;
+                        }
+                        tc5::fence_after();
+                        const uint64_t da = da0 + s * (kStageBytes >> 4), db = db0 + s * (kStageBytes >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk) {
-                        const uint64_t da = tc5::desc_k_major(st + kk * 32);
-                        const uint64_t db = bmn ? tc5::desc_mn_major(st + kABytes + kk * 2048, 64 * kBK * 2)
-                                                : tc5::desc_k_major(st + kABytes + kk * 32);
-                        tc5::mma_pair(d, da, db, idesc, kb != 0 || kk != 0);
+                        for (int kk = 0; kk < kBK / 16; ++kk) {
+                            tc5::mma_pair(d, da + kk * sa, db + kk * sb, idesc, accumulate);
+                            accumulate = 1;
+                        }
+                        tc5::commit_both(empty(s));  // both CTAs' slab is free once these have read it
+                        if (++s == kStages) {
+                            s = 0;
+                            phase ^= 1;
+                        }
                     }
-                    tc5::commit_both(empty(s));  // both CTAs' slab is free once these have read it
+                };
+                for (int pass = 0; pass < n.passes; ++pass) {
+                    const int first = min(n.a_above, n.b_above), second = max(n.a_above, n.b_above);
+                    run(0, first, false, false);
+                    run(first, second, n.a_above <= first, n.b_above <= first);
+                    run(second, n.heads, true, true);
                 }
                 tc5::commit_both(acc_full(a));
                 if (!ok) break;
@@ -437,11 +494,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
             if (!mbar_wait(drain, 0)) record_timeout(g.status);
         }
     } else {
-        const int quarter = warp & 3;  // TMEM lanes 32 * quarter .. + 31
-        // this warp's boxes, first and second of each turn
-        auto box = [&](int turn, int k) { return kOutAt + (uint32_t)(quarter * 4 + turn * 2 + k) * kBox; };
-        int i = 0, turns = 0;        // groups done
-        int loads = 0, issued = 0;   // boxes of S waited for; loaded (lane 0)
+        const int quarter = warp & 3, me = warp - 2;  // TMEM lanes 32 * quarter .. + 31
+        const int group0 = me >> 2;                   // every other 64 columns from this on
+        auto box = [&](int k) { return kOutAt + (uint32_t)(me * 2 + k) * kBox; };
+        int i = 0;
+        uint32_t s_phase = 0;  // bit k: the phase of s_full(me, k)
         bool ok = true;
         for (int t = pair; t < g.tiles && ok; t += npairs, ++i) {
             const int a = i & 1;
@@ -452,24 +509,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
             const bool tail = x.kind == kApply && !finish && ((g.tails >> (x.step + 1)) & 1);
             const bool out_bf16 = finish && g.bf16, turned = finish && g.transposed, plain = finish && g.O;
             const int row0 = x.tm * kTileM + 128 * (int)rank + 32 * quarter, row = row0 + lane, col0 = x.tn * bn;
-            // 64-column groups of this warp inside the output
+            // 64-column groups of the tile inside the output
             const int groups = row0 >= g.r ? 0 : min(bn / 64, (N - col0 + 63) / 64);
-            const bool mirror = x.kind != kApply && col0 + bn <= x.tm * kTileM;  // below the diagonal tile
             const float rho = x.step == 0 ? g.rho[z] : 1.f;
             const float beta = g.coef[3 * x.step + 1], diag = g.coef[3 * x.step] * kScaleS;
             const float alpha = x.kind == kGram ? kScaleS / (kScaleX * kScaleX) * rho * rho
                                 : poly          ? g.coef[3 * x.step + 2] / kScaleS
                                                 : rho / kScaleS / (finish ? kScaleX : 1.f);
-            auto fetch_s = [&](int q, int turn) {  // lane 0: S's box q into the turn's first box
-                const uint32_t bar = s_full(quarter, issued & 1);
-                mbar_expect_tx(bar, kBox);
-                tma_load_3d(base + box(turn & 1, 0), &maps.in, col0 + 64 * q, row0, z, bar);
-                ++issued;
-            };
+            // S's boxes come into this warp's, the first group's and the second's
+            const bool with_s = poly && group0 < groups;
             bool come = true;
-            if (poly && groups && lane == 0) {
+            if (with_s && lane == 0) {
                 come = wait_done(g, z, x.before);
-                if (come) fetch_s(0, turns);
+                for (int q = group0, k = 0; q < groups && come; q += 2, ++k) {
+                    mbar_expect_tx(s_full(me, k), kBox);
+                    tma_load_3d(base + box(k), &maps.in, col0 + 64 * q, row0, z, s_full(me, k));
+                }
             }
             bool filled = false;
             for (int tries = 0; tries < kPatience && !filled && !aborted(); ++tries)
@@ -481,27 +536,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
             ok = __all_sync(~0u, ok && !aborted());
             tc5::fence_after();
             const uint32_t addr = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(a * 256);
+            int k = 0;
 #pragma unroll 1
-            for (int q = 0; q < groups && ok; ++q, ++turns) {
-                const int k = turns & 1;
+            for (int q = group0; q < groups; q += 2, ++k) {
                 const int col = col0 + 64 * q;
-                unsigned char *const first = smem + box(k, 0), *const second = smem + box(k, 1);
-                if (poly) {
-                    if (lane == 0 && q + 1 < groups) {
-                        bulk_wait_read<0>();  // the other box's last store, the group before
-                        fetch_s(q + 1, turns + 1);
-                    }
-                    ok = __all_sync(~0u, mbar_wait(s_full(quarter, loads & 1), (loads >> 1) & 1));
-                    ++loads;
-                    if (!ok) {
+                if (with_s) {  // also where the tile is given up: nothing may be in flight at the end
+                    const bool here = __all_sync(~0u, come && mbar_wait(s_full(me, k), (s_phase >> k) & 1));
+                    s_phase ^= 1u << k;
+                    if (!here) {
                         if (lane == 0) fail();
-                        break;
+                        ok = false;
                     }
-                } else {
-                    // the boxes' last stores, two groups ago, have been read
-                    if (lane == 0) bulk_wait_read<1>();
+                } else if (tail && k) {
+                    if (lane == 0) bulk_wait_read<0>();  // both boxes anew
                     __syncwarp();
                 }
+                if (!ok) continue;
+                // the output's box, and the tail's
+                unsigned char *const first = smem + box(tail ? 0 : k), *const second = smem + box(1);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     uint32_t v[32];
@@ -547,16 +599,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
 #pragma unroll
                         for (int p = 0; p < 4; ++p)
                             *piece(first, p) = make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
-                    }
-                    if (mirror || turned) {
-                        // column j of the warp's rows as row j of the second box
-                        uint16_t *b = reinterpret_cast<uint16_t *>(second) + 32 * half * 32 + lane;
+                    } else {
+                        // column j of the warp's rows as row j of the box
+                        uint16_t *b = reinterpret_cast<uint16_t *>(first) + 32 * half * 32 + lane;
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             b[(2 * j) * 32] = (uint16_t)w[j];
                             b[(2 * j + 1) * 32] = (uint16_t)(w[j] >> 16);
                         }
-                    } else if (tail) {
+                    }
+                    if (tail) {
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
                             uint32_t lo[4];
@@ -574,10 +626,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if (!turned) tma_store_3d(&maps.out, col, row0, z, base + box(k, 0));
-                    if (mirror || turned)
-                        tma_store_3d(&maps.second, row0, col, z, base + box(k, 1));
-                    else if (tail) tma_store_3d(&maps.second, col, row0, z, base + box(k, 1));
+                    const uint32_t from = base + box(tail ? 0 : k);
+                    if (turned) tma_store_3d(&maps.out, row0, col, z, from);
+                    else tma_store_3d(&maps.out, col, row0, z, from);
+                    if (tail) tma_store_3d(&maps.tail, col, row0, z, base + box(1));
                     bulk_commit();
                 }
             }
@@ -592,12 +644,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
                 asm volatile("red.release.gpu.global.add.u32 [%0], %1;\n" ::"l"(g.done + z), "r"(1u) : "memory");
             }
         }
-        if (lane == 0) {
-            bulk_wait<0>();
-            // given up: loads of S in flight land before shared memory goes away
-            for (; loads < issued; ++loads)
-                if (!mbar_wait(s_full(quarter, loads & 1), (loads >> 1) & 1)) record_timeout(g.status);
-        }
+        if (lane == 0) bulk_wait<0>();
     }
     tc5::fence_before();
     __syncthreads();
@@ -685,7 +732,7 @@ int most_pairs(int *out) {
         if (e != cudaSuccess) return cuda_status(e);
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(192);
+        cfg.blockDim = dim3(kProductThreads);
         cfg.dynamicSmemBytes = kSmemBytes;
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeClusterDimension;
@@ -808,30 +855,24 @@ int run(const OrthArgs &a, unsigned long long tails, cudaStream_t st) {
         if (k && a.steps == 1) break;
         // S = X X^T
         map(&gram[k].a, mX, kBK, 128);
-        map(&gram[k].b_hi, mX, kBK, g.sym.bn / 2);
-        gram[k].b_lo = gram[k].b_hi;
-        if (k == 0) {
-            map(&gram[0].out, mS, 64, 32);
-            map(&gram[0].second, mS, 32, 64, false);
-        } else {
-            gram[1].out = gram[0].out;
-            gram[1].second = gram[0].second;
-        }
-        gram[k].in = gram[k].out;
+        map(&gram[k].b, mX, kBK, g.sym.bn / 2);
+        if (k == 0) map(&gram[0].out, mS, 64, 32);
+        else gram[1].out = gram[0].out;
         // X = C X, from buffer k to the other
-        map(&apply[k].b_hi, mX, 64, kBK);
+        map(&apply[k].b, mX, 64, kBK);
         map(&apply[k].b_lo, mL, 64, kBK);
         map(&apply[k ^ 1].out, mX, 64, 32);
-        map(&apply[k ^ 1].second, mL, 64, 32);
+        map(&apply[k ^ 1].tail, mL, 64, 32);
     }
     map(&poly.a, mS, kBK, 128);
-    map(&poly.b_hi, mS, kBK, g.sym.bn / 2);
-    poly.b_lo = poly.b_hi;
+    map(&poly.above, mS, 64, kBK);
+    map(&poly.b, mS, kBK, g.sym.bn / 2);
     map(&poly.out, mC, 64, 32);
-    map(&poly.second, mC, 32, 64, false);
     poly.in = gram[0].out;
     map(&apply[0].a, mC, kBK, 128);
+    map(&apply[0].above, mC, 64, kBK);
     apply[1].a = apply[0].a;
+    apply[1].above = apply[0].above;
     // the last product writes O, by TMA where its rows start on 16-byte boundaries
     Maps &finish = g.finish;
     finish = apply[(a.steps - 1) & 1];
@@ -841,9 +882,7 @@ int run(const OrthArgs &a, unsigned long long tails, cudaStream_t st) {
         // strides of a single row or matrix are of no account, but a map needs valid ones
         const int64_t ld = a.m > 1 ? a.ldo : up8(a.n), so = a.batch > 1 ? a.strideO : up8(a.m * ld);
         const Matrix mO = {a.O, a.n, a.m, ld, so};
-        map(tall ? &finish.second : &finish.out, mO, tall ? 32 : 64, tall ? 64 : 32, !tall);
-        if (tall) finish.out = finish.second;
-        else finish.second = finish.out;
+        map(&finish.out, mO, tall ? 32 : 64, tall ? 64 : 32, !tall);
     }
 
     if (rc) return rc;
@@ -856,7 +895,7 @@ int run(const OrthArgs &a, unsigned long long tails, cudaStream_t st) {
     const int64_t first = (int64_t)(g.sym.per > g.app.per ? g.sym.per : g.app.per) * a.batch;  // tiles at one time
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (unsigned)(first < pairs ? first : pairs));
-    cfg.blockDim = dim3(192);
+    cfg.blockDim = dim3(kProductThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = st;
     cudaLaunchAttribute at[1];

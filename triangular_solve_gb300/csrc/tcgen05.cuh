@@ -32,10 +32,11 @@ __device__ __forceinline__ uint64_t desc_mn_major(uint32_t saddr, uint32_t span)
     d |= (uint64_t)2 << 61;
     return d;
 }
-// Instruction descriptor: f16 operands, f32 accumulator, A K-major.
-__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool b_mn_major) {
+// Instruction descriptor: f16 operands, f32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool a_mn_major, bool b_mn_major) {
     return (1u << 4)                         // D format f32
-           | ((b_mn_major ? 1u : 0u) << 16)  // B MN-major
+           | ((a_mn_major ? 1u : 0u) << 15)
+           | ((b_mn_major ? 1u : 0u) << 16)
            | ((uint32_t)(n >> 3) << 17)      // N / 8
            | ((uint32_t)(m >> 4) << 24);     // M / 16; A and B format f16 are 0
 }
