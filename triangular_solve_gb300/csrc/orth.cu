@@ -178,10 +178,9 @@ struct Maps {
     CUtensorMap a, above, b, b_lo, out, tail, in;
 };
 
-// Tiles of one kind of product: bn columns wide (128 or 256), per of them a
-// matrix.
+// Tiles of one kind of product, `per` of them a matrix.
 struct Tiling {
-    int bn, tiles_m, tiles_n, per;
+    int tiles_m, tiles_n, per;
 };
 
 // All products of a call.  Tiles are numbered step by step, product by
@@ -189,13 +188,14 @@ struct Tiling {
 struct Schedule {
     Maps gram[2], poly, apply[2], finish;  // by the buffer that holds X_k
     Tiling sym, app;
+    int bn;                     // columns of a tile: 128 or 256
     int r, c, batch, steps, tiles;
     int transposed, bf16;       // of O
     void *O;                    // stored element by element; null: through the maps
     int64_t ldo, strideO;
     unsigned long long tails;   // bit k: X_k has a tail
     const float *rho;           // per matrix
-    unsigned *done;             // per matrix: warps that have stored a tile; then the abort word
+    unsigned *done;             // per matrix: CTAs' shares of its tiles that are stored; then the abort word
     int *status;
     float coef[3 * kMaxSteps];
 };
@@ -203,19 +203,17 @@ struct Schedule {
 constexpr int kTileM = 256, kBK = 64;
 constexpr uint32_t kABytes = 128 * kBK * 2;  // 128 rows of A per CTA
 constexpr uint32_t kHalfBytes = 64 * kBK * 2;  // a box of 64 x 64
-constexpr uint32_t kStageBytes = 2 * kABytes;
-constexpr int kStages = 5;
+constexpr uint32_t kRingBytes = 6 * 2 * kABytes;   // 6 stages of 256-column tiles, 8 of 128-column ones
+constexpr int kMostStages = 8;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kBox = 32 * 64 * 2;       // bytes of a box of the output
-constexpr int kOutWarps = 8;                 // that empty the accumulators
-constexpr uint32_t kOutAt = kStages * kStageBytes;  // two output boxes for each of them
-constexpr uint32_t kBarsAt = kOutAt + 2 * kOutWarps * kBox;
-constexpr uint32_t kTmemAt = kBarsAt + 8u * (2 * kStages + 5 + 2 * kOutWarps);
-constexpr int kProductThreads = 32 * (2 + kOutWarps);
+constexpr uint32_t kBox = 32 * 64 * 2;             // bytes of a box of the output
+constexpr int kOutWarps = 8;                       // that empty the accumulators, a box each
+constexpr uint32_t kBarsAt = kRingBytes + kOutWarps * kBox;
+constexpr uint32_t kTmemAt = kBarsAt + 8u * (2 * kMostStages + 9 + kOutWarps);
+constexpr int kProductThreads = 32 * (3 + kOutWarps);
 constexpr size_t kSmemBytes = 1024 + kBarsAt + 512;
 static_assert(kTmemAt + 4 <= kBarsAt + 512 && kSmemBytes <= 227 * 1024, "shared memory");
-constexpr int kPatience = 4;                 // full waits for what itself waits for another product
-constexpr unsigned kWarpsATile = 2 * kOutWarps;  // that store it, of both CTAs
+constexpr int kPatience = 4;                       // full waits for what itself waits for another product
 
 __device__ __forceinline__ uint32_t pack_half(float x, float y) {
     const __half2 h = __floats2half2_rn(x, y);
@@ -230,7 +228,7 @@ __device__ __forceinline__ uint32_t pack_out(float x, float y, bool bf16) {
 // One tile of the schedule.
 struct Tile {
     int step, kind, z, tm, tn;
-    unsigned before;  // warps' stores of this matrix's earlier products
+    unsigned before;  // CTAs' shares of this matrix's earlier products
 };
 __device__ __forceinline__ Tile tile_at(const Schedule &g, int t) {
     const int sym = g.sym.per * g.batch, app = g.app.per * g.batch;
@@ -242,10 +240,10 @@ __device__ __forceinline__ Tile tile_at(const Schedule &g, int t) {
     const Tiling &k = x.kind == kApply ? g.app : g.sym;
     x.z = u / k.per;
     u -= x.z * k.per;
-    x.before = kWarpsATile * (unsigned)(x.step * (2 * g.sym.per + g.app.per) + x.kind * g.sym.per);
+    x.before = 2u * (unsigned)(x.step * (2 * g.sym.per + g.app.per) + x.kind * g.sym.per);
     if (x.kind != kApply) {
         // row tile tm has the column tiles up to the diagonal's
-        const int more = kTileM / k.bn;
+        const int more = kTileM / g.bn;
         x.tm = 0;
         int width = min(more, k.tiles_n);
         while (u >= width) {
@@ -273,8 +271,8 @@ __device__ __forceinline__ unsigned load_acquire(const unsigned *p) {
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];\n" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
-// Until `need` warps have stored their tiles of matrix z, with what they
-// stored visible to this thread's later TMA loads; false when the wait
+// Until `need` shares of matrix z's tiles are stored, with what was stored
+// visible to this thread's later TMA loads; false when the wait
 // expired or another CTA gave up.
 __device__ __forceinline__ bool wait_done(const Schedule &g, int z, unsigned need) {
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
@@ -292,11 +290,13 @@ __device__ __forceinline__ bool wait_done(const Schedule &g, int z, unsigned nee
 // ring of slabs of K = 64), warp 1 of the even CTA issues the MMAs, warps
 // 2..9 empty the accumulators (two in TMEM, so a tile's way out runs under
 // the next one's MMAs): 64 columns at a time through shared memory, from
-// where TMA stores them.
+// where TMA stores them.  Warp 10 announces the tile.
 //
-// A product waits for the one before it matrix by matrix: the warps that
-// store a tile count themselves in done[z] once their stores are complete,
-// and a tile's loads wait for the count of its matrix's earlier products.
+// A product waits for the one before it matrix by matrix: each CTA counts its
+// half of a tile in done[z] once its stores are complete, and a tile's loads
+// wait for the count of its matrix's earlier products.  (The count is a
+// release at GPU scope, which takes longer than a tile's way out; hence a
+// warp for it.)
 // Every tile comes after those it waits for, in the order in which each pair
 // takes its tiles, and the launch is cooperative, so the waits end; they are
 // bounded all the same.
@@ -312,11 +312,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     unsigned char *const smem = smem_raw + (base - raw);
     const uint32_t bars = base + kBarsAt;
     auto full = [&](int s) { return bars + 8u * s; };
-    auto empty = [&](int s) { return bars + 8u * (kStages + s); };
-    auto acc_full = [&](int a) { return bars + 8u * (2 * kStages + a); };
-    auto acc_empty = [&](int a) { return bars + 8u * (2 * kStages + 2 + a); };
-    const uint32_t drain = bars + 8u * (2 * kStages + 4);
-    auto s_full = [&](int w, int k) { return bars + 8u * (2 * kStages + 5 + 2 * w + k); };  // kPoly: S has come
+    auto empty = [&](int s) { return bars + 8u * (kMostStages + s); };
+    auto acc_full = [&](int a) { return bars + 8u * (2 * kMostStages + a); };
+    auto acc_empty = [&](int a) { return bars + 8u * (2 * kMostStages + 2 + a); };
+    auto stored = [&](int a) { return bars + 8u * (2 * kMostStages + 4 + a); };
+    auto announced = [&](int a) { return bars + 8u * (2 * kMostStages + 6 + a); };
+    const uint32_t drain = bars + 8u * (2 * kMostStages + 8);
+    auto s_full = [&](int w) { return bars + 8u * (2 * kMostStages + 9 + w); };  // kPoly: S has come
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kTmemAt);
     __shared__ int abort_flag;
 
@@ -324,13 +326,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     const uint32_t rank = cluster::rank();
     const bool leader = rank == 0;
     const int pair = (int)blockIdx.x >> 1, npairs = (int)gridDim.x >> 1;
+    const int bn = g.bn, stages = bn == 256 ? 6 : 8;
+    const uint32_t stage_bytes = kRingBytes / stages;
     // The slabs of a tile: `heads` with X's head, as many again with its tail;
     // of each kind, those from `a_above` (`b_above`) on take their part of A
     // (B) from below the diagonal, or, C X's B, all as columns.
     struct Slabs {
         int heads, passes, a_above, b_above;
     };
-    auto slabs_of = [&](const Tile &x, int bn) {
+    auto slabs_of = [&](const Tile &x) {
         Slabs s;
         s.heads = ((x.kind == kGram ? g.c : g.r) + kBK - 1) / kBK;
         s.passes = x.kind == kApply && ((g.tails >> x.step) & 1) ? 2 : 1;
@@ -343,17 +347,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(acc_full(a), 1);
-            mbar_init(acc_empty(a), kWarpsATile);
+            mbar_init(acc_empty(a), 2 * kOutWarps);  // in both CTAs
+            mbar_init(stored(a), kOutWarps);
+            mbar_init(announced(a), 1);
         }
         mbar_init(drain, 1);
-        for (int w = 0; w < kOutWarps; ++w)
-            for (int k = 0; k < 2; ++k) mbar_init(s_full(w, k), 1);
+        for (int w = 0; w < kOutWarps; ++w) mbar_init(s_full(w), 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 1) tc5::alloc_pair(smem_u32(tmem_slot), kTmemCols);
@@ -381,15 +386,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                     fail();
                     break;
                 }
-                const int bn = x.kind == kApply ? g.app.bn : g.sym.bn;
                 const int ya = x.tm * kTileM + 128 * (int)rank, yb = x.tn * bn + bn / 2 * (int)rank;
-                const Slabs n = slabs_of(x, bn);
+                const Slabs n = slabs_of(x);
                 const uint32_t bytes = 2 * (kABytes + bn / 2 * kBK * 2);
                 bool ok = true;
                 for (int pass = 0; pass < n.passes && ok; ++pass) {
                     const CUtensorMap *const columns = x.kind == kPoly ? &m.above : pass ? &m.b_lo : &m.b;
                     for (int kb = 0; kb < n.heads; ++kb) {
-                        if (filled == kStages) {
+                        if (filled == stages) {
                             if (!mbar_wait(empty(s), phase)) {
                                 ok = false;
                                 break;
@@ -398,7 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                             ++filled;
                         }
                         if (leader) mbar_expect_tx(full(s), bytes);
-                        const uint32_t st = base + s * kStageBytes, fb = full0 + 8 * s;
+                        const uint32_t st = base + s * stage_bytes, fb = full0 + 8 * s;
                         const int kx = kb * kBK;
                         if (kb < n.a_above) {
                             tc5::load_pair(st, &m.a, kx, ya, x.z, fb);
@@ -412,7 +416,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                             tc5::load_pair(st + kABytes, columns, yb, kx, x.z, fb);
                             if (bn == 256) tc5::load_pair(st + kABytes + kHalfBytes, columns, yb + 64, kx, x.z, fb);
                         }
-                        if (++s == kStages) {
+                        if (++s == stages) {
                             s = 0;
                             phase ^= 1;
                         }
@@ -427,8 +431,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                 // the pair's loads counted on these barriers land before shared
                 // memory goes away: the newest of each stage in use
                 for (int j = 0; j < filled; ++j) {
-                    s = s ? s - 1 : kStages - 1;
-                    if (s == kStages - 1) phase ^= 1;
+                    s = s ? s - 1 : stages - 1;
+                    if (s == stages - 1) phase ^= 1;
                     if (!mbar_wait(full(s), phase ^ 1)) record_timeout(g.status);
                 }
             }
@@ -439,8 +443,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
             uint32_t phase = 0;  // of full(s)
             for (int t = pair; t < g.tiles && !aborted(); t += npairs, ++i) {
                 const Tile x = tile_at(g, t);
-                const int bn = x.kind == kApply ? g.app.bn : g.sym.bn, a = i & 1;
-                const Slabs n = slabs_of(x, bn);
+                const int a = i & 1;
+                const Slabs n = slabs_of(x);
                 if (i >= 2 && !mbar_wait(acc_empty(a), ((i >> 1) - 1) & 1)) {
                     fail();
                     break;
@@ -468,14 +472,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                             break;
                         }
                         tc5::fence_after();
-                        const uint64_t da = da0 + s * (kStageBytes >> 4), db = db0 + s * (kStageBytes >> 4);
+                        const uint64_t da = da0 + s * (stage_bytes >> 4), db = db0 + s * (stage_bytes >> 4);
 #pragma unroll
                         for (int kk = 0; kk < kBK / 16; ++kk) {
                             tc5::mma_pair(d, da + kk * sa, db + kk * sb, idesc, accumulate);
                             accumulate = 1;
                         }
                         tc5::commit_both(empty(s));  // both CTAs' slab is free once these have read it
-                        if (++s == kStages) {
+                        if (++s == stages) {
                             s = 0;
                             phase ^= 1;
                         }
@@ -493,18 +497,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
             tc5::commit_local(drain);
             if (!mbar_wait(drain, 0)) record_timeout(g.status);
         }
+    } else if (warp == 2 + kOutWarps) {
+        if (lane == 0) {
+            int i = 0;
+            for (int t = pair; t < g.tiles && !aborted(); t += npairs, ++i) {
+                const Tile x = tile_at(g, t);
+                bool all = false;
+                for (int tries = 0; tries < kPatience && !all && !aborted(); ++tries)
+                    all = mbar_wait(stored(i & 1), (i >> 1) & 1);
+                if (!all) {
+                    fail();
+                    break;
+                }
+                asm volatile("fence.proxy.async;\n" ::: "memory");
+                asm volatile("red.release.gpu.global.add.u32 [%0], %1;\n" ::"l"(g.done + x.z), "r"(1u) : "memory");
+                mbar_arrive(announced(i & 1));
+            }
+        }
     } else {
         const int quarter = warp & 3, me = warp - 2;  // TMEM lanes 32 * quarter .. + 31
         const int group0 = me >> 2;                   // every other 64 columns from this on
-        auto box = [&](int k) { return kOutAt + (uint32_t)(me * 2 + k) * kBox; };
+        const uint32_t box = kRingBytes + (uint32_t)me * kBox;
+        unsigned char *const out = smem + box;
         int i = 0;
-        uint32_t s_phase = 0;  // bit k: the phase of s_full(me, k)
+        uint32_t s_phase = 0;
         bool ok = true;
         for (int t = pair; t < g.tiles && ok; t += npairs, ++i) {
             const int a = i & 1;
             const Tile x = tile_at(g, t);
             const Maps &maps = maps_of(g, x);
-            const int z = x.z, bn = x.kind == kApply ? g.app.bn : g.sym.bn, N = x.kind == kApply ? g.c : g.r;
+            const int z = x.z, N = x.kind == kApply ? g.c : g.r;
             const bool poly = x.kind == kPoly, finish = x.kind == kApply && x.step + 1 == g.steps;
             const bool tail = x.kind == kApply && !finish && ((g.tails >> (x.step + 1)) & 1);
             const bool out_bf16 = finish && g.bf16, turned = finish && g.transposed, plain = finish && g.O;
@@ -516,15 +538,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
             const float alpha = x.kind == kGram ? kScaleS / (kScaleX * kScaleX) * rho * rho
                                 : poly          ? g.coef[3 * x.step + 2] / kScaleS
                                                 : rho / kScaleS / (finish ? kScaleX : 1.f);
-            // S's boxes come into this warp's, the first group's and the second's
-            const bool with_s = poly && group0 < groups;
+            auto fetch_s = [&](int q) {  // lane 0: S's box of group q, into this warp's
+                mbar_expect_tx(s_full(me), kBox);
+                tma_load_3d(base + box, &maps.in, col0 + 64 * q, row0, z, s_full(me));
+            };
             bool come = true;
-            if (with_s && lane == 0) {
+            if (poly && group0 < groups && lane == 0) {
                 come = wait_done(g, z, x.before);
-                for (int q = group0, k = 0; q < groups && come; q += 2, ++k) {
-                    mbar_expect_tx(s_full(me, k), kBox);
-                    tma_load_3d(base + box(k), &maps.in, col0 + 64 * q, row0, z, s_full(me, k));
-                }
+                if (come) fetch_s(group0);
             }
             bool filled = false;
             for (int tries = 0; tries < kPatience && !filled && !aborted(); ++tries)
@@ -536,46 +557,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
             ok = __all_sync(~0u, ok && !aborted());
             tc5::fence_after();
             const uint32_t addr = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(a * 256);
-            int k = 0;
+            // the accumulator goes back once this warp has read its last columns
+            const int last = group0 < groups ? group0 + ((groups - 1 - group0) & ~1) : -1;
+            auto hand_back = [&]() {
+                tc5::fence_before();
+                __syncwarp();
+                if (lane == 0) tc5::arrive_cluster_relaxed(cluster::map(acc_empty(a), 0));
+            };
+            if (last < 0) hand_back();
+            bool own = true;  // nothing reads or writes the box
 #pragma unroll 1
-            for (int q = group0; q < groups; q += 2, ++k) {
+            for (int q = group0; q < groups; q += 2) {
                 const int col = col0 + 64 * q;
-                if (with_s) {  // also where the tile is given up: nothing may be in flight at the end
-                    const bool here = __all_sync(~0u, come && mbar_wait(s_full(me, k), (s_phase >> k) & 1));
-                    s_phase ^= 1u << k;
+                if (!own) {
+                    if (lane == 0) {
+                        bulk_wait_read<0>();
+                        if (poly) fetch_s(q);
+                    }
+                    __syncwarp();
+                }
+                if (poly) {  // also where the tile is given up: nothing may be in flight at the end
+                    const bool here = __all_sync(~0u, come && mbar_wait(s_full(me), s_phase));
+                    s_phase ^= 1;
                     if (!here) {
                         if (lane == 0) fail();
                         ok = false;
                     }
-                } else if (tail && k) {
-                    if (lane == 0) bulk_wait_read<0>();  // both boxes anew
-                    __syncwarp();
                 }
-                if (!ok) continue;
-                // the output's box, and the tail's
-                unsigned char *const first = smem + box(tail ? 0 : k), *const second = smem + box(1);
+                if (!ok) break;
+                uint32_t lo[2][16];
+                // 16-byte piece p of this thread's row of the box, under the swizzle
+                auto piece = [&](int p) {
+                    return reinterpret_cast<uint4 *>(out + lane * 128 + (p ^ (lane & 7)) * 16);
+                };
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     uint32_t v[32];
                     tc5::read_32(v, addr + 64 * q + 32 * half);
+                    if (half && q == last) hand_back();
                     float o[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) o[j] = alpha * __uint_as_float(v[j]);
-                    // 16-byte piece p of this thread's row, under the swizzle
-                    auto piece = [&](unsigned char *b, int p) {
-                        return reinterpret_cast<uint4 *>(b + lane * 128 + ((4 * half + p) ^ (lane & 7)) * 16);
-                    };
                     if (poly) {
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
-                            const uint4 w = *piece(first, p);
+                            const uint4 w = *piece(4 * half + p);
                             const __half *h = reinterpret_cast<const __half *>(&w);
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                o[8 * p + j] = fmaf(beta, __half2float(h[j]), o[8 * p + j]);
-                                if (col + 32 * half + 8 * p + j == row) o[8 * p + j] += diag;
-                            }
+                            for (int j = 0; j < 8; ++j) o[8 * p + j] = fmaf(beta, __half2float(h[j]), o[8 * p + j]);
                         }
+                        const int at = row - col - 32 * half;  // the diagonal's place
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j == at) o[j] += diag;
                     }
                     if (plain) {
                         const int64_t zo = z * g.strideO;
@@ -598,10 +632,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                     if (!turned) {
 #pragma unroll
                         for (int p = 0; p < 4; ++p)
-                            *piece(first, p) = make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
+                            *piece(4 * half + p) = make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
                     } else {
                         // column j of the warp's rows as row j of the box
-                        uint16_t *b = reinterpret_cast<uint16_t *>(first) + 32 * half * 32 + lane;
+                        uint16_t *b = reinterpret_cast<uint16_t *>(out) + 32 * half * 32 + lane;
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             b[(2 * j) * 32] = (uint16_t)w[j];
@@ -610,15 +644,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                     }
                     if (tail) {
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) {
-                            uint32_t lo[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const __half2 hi = *reinterpret_cast<const __half2 *>(&w[4 * p + j]);
-                                lo[j] = pack_half(o[8 * p + 2 * j] - __low2float(hi),
-                                                  o[8 * p + 2 * j + 1] - __high2float(hi));
-                            }
-                            *piece(second, p) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        for (int j = 0; j < 16; ++j) {
+                            const __half2 hi = *reinterpret_cast<const __half2 *>(&w[j]);
+                            lo[half][j] = pack_half(o[2 * j] - __low2float(hi), o[2 * j + 1] - __high2float(hi));
                         }
                     }
                 }
@@ -626,23 +654,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    const uint32_t from = base + box(tail ? 0 : k);
-                    if (turned) tma_store_3d(&maps.out, row0, col, z, from);
-                    else tma_store_3d(&maps.out, col, row0, z, from);
-                    if (tail) tma_store_3d(&maps.tail, col, row0, z, base + box(1));
+                    if (turned) tma_store_3d(&maps.out, row0, col, z, base + box);
+                    else tma_store_3d(&maps.out, col, row0, z, base + box);
                     bulk_commit();
                 }
+                if (tail) {
+                    if (lane == 0) bulk_wait_read<0>();
+                    __syncwarp();
+#pragma unroll
+                    for (int p = 0; p < 8; ++p)
+                        *piece(p) = make_uint4(lo[p / 4][4 * (p % 4)], lo[p / 4][4 * (p % 4) + 1],
+                                               lo[p / 4][4 * (p % 4) + 2], lo[p / 4][4 * (p % 4) + 3]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_3d(&maps.tail, col, row0, z, base + box);
+                        bulk_commit();
+                    }
+                }
+                own = false;
             }
-            // every TMEM read of accumulator a is done: hand it back
-            tc5::fence_before();
-            __syncwarp();
             if (lane == 0) {
-                tc5::arrive_cluster(cluster::map(acc_empty(a), 0));
-                // the stores are complete: count this warp
-                bulk_wait<0>();
-                asm volatile("fence.proxy.async;\n" ::: "memory");
-                asm volatile("red.release.gpu.global.add.u32 [%0], %1;\n" ::"l"(g.done + z), "r"(1u) : "memory");
+                bulk_wait<0>();  // the stores are complete
+                // not before the tile two back has been announced
+                if (i >= 2 && !mbar_wait(announced(a), ((i >> 1) - 1) & 1)) fail();
+                mbar_arrive(stored(a));
             }
+            __syncwarp();
         }
         if (lane == 0) bulk_wait<0>();
     }
@@ -750,29 +788,35 @@ int most_pairs(int *out) {
     return TRSM_SUCCESS;
 }
 
-// Tiles of r x N products for every matrix (symmetric: N = r, down to the
-// diagonal's): 128 columns wide where that takes less time.  A pair's tile
-// costs its width and about 32 columns' time besides; one matrix's product
-// takes whole rounds of the pairs, those of several run into each other.
-Tiling tiling(int64_t r, int64_t N, bool symmetric, int64_t batch, int pairs) {
-    Tiling best = {};
-    double least = 0;
-    for (int bn = 256; bn >= 128; bn /= 2) {
-        Tiling t = {bn, (int)((r + kTileM - 1) / kTileM), (int)((N + bn - 1) / bn), 0};
-        if (symmetric) {
-            for (int tm = 0; tm < t.tiles_m; ++tm) {
-                const int w = kTileM / bn * (tm + 1);
-                t.per += w < t.tiles_n ? w : t.tiles_n;
-            }
-        } else {
-            t.per = t.tiles_m * t.tiles_n;
+Tiling tiling(int64_t r, int64_t N, bool symmetric, int bn) {
+    Tiling t = {(int)((r + kTileM - 1) / kTileM), (int)((N + bn - 1) / bn), 0};
+    if (!symmetric) {
+        t.per = t.tiles_m * t.tiles_n;
+    } else {
+        for (int tm = 0; tm < t.tiles_m; ++tm) {
+            const int w = kTileM / bn * (tm + 1);
+            t.per += w < t.tiles_n ? w : t.tiles_n;
         }
-        double rounds = (double)t.per * batch / pairs;
-        if (batch == 1) rounds = ceil(rounds);
-        if (rounds < 1) rounds = 1;
-        const double cost = rounds * (bn + 32);
-        if (!best.bn || cost < least) {
-            best = t;
+    }
+    return t;
+}
+
+// Columns of a tile, 256 or 128: whichever takes less time by the time of a
+// slab of K (0.31 us of a 256 x 256 tile, 0.20 of a 256 x 128 one) and of a
+// product's way out (3 and 2 us).  One matrix's product takes whole rounds of
+// the CTA pairs; those of several run into each other.
+int choose_bn(int64_t r, int64_t c, int64_t batch, int pairs) {
+    double least = 0;
+    int best = 256;
+    for (int bn = 256; bn >= 128; bn /= 2) {
+        auto rounds = [&](const Tiling &t) {
+            const double n = (double)t.per * batch / pairs;
+            return n < 1 ? 1.0 : batch == 1 ? ceil(n) : n;
+        };
+        const double sym = rounds(tiling(r, r, true, bn)), app = rounds(tiling(r, c, false, bn));
+        const double cost = (bn == 256 ? 0.31 : 0.20) / kBK * (sym * (c + r) + app * r) + (bn == 256 ? 9 : 6);
+        if (bn == 256 || cost < least) {
+            best = bn;
             least = cost;
         }
     }
@@ -833,8 +877,9 @@ int run(const OrthArgs &a, unsigned long long tails, cudaStream_t st) {
     g.c = (int)w.c;
     g.batch = (int)a.batch;
     g.steps = a.steps;
-    g.sym = tiling(w.r, w.r, true, a.batch, pairs);
-    g.app = tiling(w.r, w.c, false, a.batch, pairs);
+    g.bn = choose_bn(w.r, w.c, a.batch, pairs);
+    g.sym = tiling(w.r, w.r, true, g.bn);
+    g.app = tiling(w.r, w.c, false, g.bn);
     const int64_t tiles = (2 * (int64_t)g.sym.per + g.app.per) * a.batch * a.steps;
     if (tiles > 0x0fffffff) return -11;
     g.tiles = (int)tiles;
@@ -855,7 +900,7 @@ int run(const OrthArgs &a, unsigned long long tails, cudaStream_t st) {
         if (k && a.steps == 1) break;
         // S = X X^T
         map(&gram[k].a, mX, kBK, 128);
-        map(&gram[k].b, mX, kBK, g.sym.bn / 2);
+        map(&gram[k].b, mX, kBK, g.bn / 2);
         if (k == 0) map(&gram[0].out, mS, 64, 32);
         else gram[1].out = gram[0].out;
         // X = C X, from buffer k to the other
@@ -866,7 +911,7 @@ int run(const OrthArgs &a, unsigned long long tails, cudaStream_t st) {
     }
     map(&poly.a, mS, kBK, 128);
     map(&poly.above, mS, 64, kBK);
-    map(&poly.b, mS, kBK, g.sym.bn / 2);
+    map(&poly.b, mS, kBK, g.bn / 2);
     map(&poly.out, mC, 64, 32);
     poly.in = gram[0].out;
     map(&apply[0].a, mC, kBK, 128);
