@@ -16,12 +16,13 @@
 // (forward 3 elements a token and channel, backward 5, or 6 in the sigmoid
 // form) and does a few operations on each.
 //
-// Layout.  A CTA of 256 threads takes `VEC` channels per lane and `LANES`
-// lanes side by side (128 bytes of a row with 16-byte vectors), and 256 /
-// LANES time slots of ROWS consecutive tokens each.  Every thread copies its
-// own tokens into shared memory ahead of time (cp.async, so no registers and
-// no block barrier are spent on it) and walks them twice from there; they are
-// read from memory once.  A cluster of 1..8 CTAs takes consecutive stretches
+// Layout.  A CTA of 256 threads takes 16 bytes of channels per lane and 8
+// lanes side by side, and 32 time slots of ROWS consecutive tokens each.
+// Every thread copies its own tokens into shared memory ahead of time
+// (cp.async, so no registers and no block barrier are spent on it) and walks
+// them twice from there; they are read from memory once.  Rows that do not
+// start on 16-byte boundaries are copied as the whole 16-byte pieces that they
+// touch, and shifted into place when they are read.  A cluster of 1..8 CTAs takes consecutive stretches
 // of the same channels and sequence and steps along the sequence; each step
 // composes the warps' pairs in shared memory and the CTAs' pairs through
 // distributed shared memory.  There is no flag or wait in global memory, and
@@ -64,7 +65,7 @@ __device__ __forceinline__ void round_pair(float lo, float hi, uint32_t &w, __nv
     w = *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// VEC elements of T as one access (VEC * sizeof(T) is 16, or VEC = 1).
+// VEC elements of T, aligned as one access.
 template <typename T, int VEC> struct alignas(VEC * sizeof(T)) Pack {
     T v[VEC];
 };
@@ -222,18 +223,31 @@ __device__ __forceinline__ Walk<T> walk(const LinrecRows &r, const Sequence &s, 
     return {first, r.st};
 }
 
+// First byte of a tensor, and the one past its last.
+template <typename T> __device__ __forceinline__ const char *rows_begin(const LinrecRows &r, const LinrecArgs &g) {
+    const int64_t b = g.offsets ? 0 : min((int64_t)0, (g.batch - 1) * r.sb), t = min((int64_t)0, (g.T - 1) * r.st);
+    return static_cast<const char *>(r.p) + (b + t) * (int64_t)sizeof(T);
+}
+template <typename T> __device__ __forceinline__ const char *rows_end(const LinrecRows &r, const LinrecArgs &g) {
+    const int64_t b = g.offsets ? 0 : max((int64_t)0, (g.batch - 1) * r.sb), t = max((int64_t)0, (g.T - 1) * r.st);
+    return static_cast<const char *>(r.p) + (b + t + g.D) * (int64_t)sizeof(T);
+}
+
 // One way to run the scan: THREADS threads, ROWS tokens a thread, STAGES
 // buffers of the gate and x (backward: dh); SIDE: the backward pass's h and x
-// are staged too, else they wait in registers.  BLOCKS: CTAs an SM should hold.
-template <int VEC_, int LANES_, int THREADS, int ROWS_, int STAGES_, bool SIDE_, int BLOCKS> struct Plan {
+// are staged too, else they wait in registers.  SHIFT: rows start anywhere, and
+// D is any.  BLOCKS: CTAs an SM should hold.
+template <int VEC_, int LANES_, int THREADS, int ROWS_, int STAGES_, bool SIDE_, bool SHIFT_, int BLOCKS> struct Plan {
     static constexpr int VEC = VEC_, LANES = LANES_, kThreads = THREADS, ROWS = ROWS_, STAGES = STAGES_, kBlocks = BLOCKS;
-    static constexpr bool SIDE = SIDE_;
+    static constexpr bool SIDE = SIDE_, SHIFT = SHIFT_;
     static constexpr int kChannels = LANES * VEC;      // channels of a CTA
     static constexpr int kSlots = THREADS / LANES;     // time slots of a CTA
     static constexpr int kStretch = kSlots * ROWS;     // tokens of a CTA in one step
     static constexpr int kParts = THREADS / kChannels, kPartSlots = kSlots / kParts;
-    static constexpr int kBufferElems = kStretch * kChannels;
+    static constexpr int kPitch = 16 * LANES + (SHIFT ? 16 : 0);  // bytes of a staged row
+    static constexpr int kBufferBytes = kStretch * kPitch;
     static_assert(THREADS % kChannels == 0 && kSlots % kParts == 0, "threads per channel");
+    static_assert(!SHIFT || SIDE, "rows to be shifted are all staged");
     // see slot_A
     static __device__ __forceinline__ int channel_at(int i) {
         constexpr int q = VEC < 4 ? VEC : 4;
@@ -243,7 +257,7 @@ template <int VEC_, int LANES_, int THREADS, int ROWS_, int STAGES_, bool SIDE_,
         return 2 * STAGES + (BWD && SIDE ? (FORM == TRSM_GATE_SIGMOID ? 2 : 1) : 0);
     }
     template <typename T, int FORM, bool BWD> static constexpr size_t smem() {
-        return (size_t)buffers<T, FORM, BWD>() * kBufferElems * sizeof(T);
+        return (size_t)buffers<T, FORM, BWD>() * kBufferBytes;
     }
 };
 
@@ -279,7 +293,9 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
     const int64_t d = c0 + col * VEC;
     const bool live = d < g.D;
     const Sequence seq = sequence(g, b);
-    const int len = live ? seq.len : 0;  // tokens this thread may touch
+    const int len = live ? seq.len : 0;  // tokens that this thread walks
+    // and copies: a piece may hold channels of the lane before only
+    const int copy_len = L::SHIFT ? seq.len : len;
 
     // each of them carries the state of its channel from step to step
     const int64_t dc = c0 + L::channel_at(place);
@@ -307,26 +323,74 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
         cluster::sync();  // every CTA's barriers exist before any signals them
     }
 
-    // this thread's place in staged buffer i, row r: mine(i)[r * kChannels]
-    auto mine = [&](int i) {
-        return reinterpret_cast<T *>(staged) + i * L::kBufferElems + slot * ROWS * kChannels + col * VEC;
+    // row r of this thread's slot in staged buffer i
+    auto staged_row = [&](int i, int r) { return staged + i * L::kBufferBytes + (slot * ROWS + r) * L::kPitch; };
+    // How far the 16 bytes that a row's part of this CTA starts in begin before it.
+    auto shift_at = [&](const Walk<const T> &w, int at) {
+        return (uint32_t)(reinterpret_cast<uintptr_t>(w.at) + (uint64_t)((int64_t)at * w.step) * sizeof(T)) & 15u;
     };
     // Copies positions base .. base + ROWS - 1 (those below `end`) into buffer i.
-    auto stage = [&](const Walk<const T> &w, int base, int end, int i) {
+    auto stage = [&](const Walk<const T> &w, const LinrecRows &rows, int base, int end, int i) {
         const T *p = w.at + base * w.step;
-        T *s = mine(i);
-        if constexpr (VEC * sizeof(T) == 16) {
+        if constexpr (!L::SHIFT) {
 #pragma unroll
             for (int r = 0; r < ROWS; ++r)
-                if (base + r < end) cp_async<16>(s + r * kChannels, p + r * w.step);
+                if (base + r < end) cp_async<16>(staged_row(i, r) + col * 16, p + r * w.step);
         } else {
-            P v[ROWS];
+            // every lane a piece, the last one also the ninth; pieces that
+            // reach over the tensor's ends element by element
+            const char *const lo = rows_begin<T>(rows, g), *const hi = rows_end<T>(rows, g);
+            const int64_t bytes = min((int64_t)kChannels, g.D - c0) * (int64_t)sizeof(T);
+#pragma unroll 2
+            for (int r = 0; r < ROWS; ++r) {
+                if (base + r >= end) break;
+                const char *row = reinterpret_cast<const char *>(p + r * w.step) - col * 16;
+                const char *first = reinterpret_cast<const char *>(reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)15);
+                unsigned char *const to = staged_row(i, r);
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r)
-                if (base + r < end) v[r] = load_pack<T, VEC>(p + r * w.step);
+                for (int q = 0; q < 2; ++q) {
+                    const int k = q ? LANES : col;
+                    const char *from = first + 16 * k;
+                    if ((q && col != LANES - 1) || from >= row + bytes) continue;
+                    if (from >= lo && from + 16 <= hi) {
+                        cp_async<16>(to + 16 * k, from);
+                    } else {
+                        for (int e = 0; e < VEC; ++e)
+                            if (from + e * sizeof(T) >= lo && from + e * sizeof(T) < hi)
+                                reinterpret_cast<T *>(to + 16 * k)[e] = reinterpret_cast<const T *>(from)[e];
+                    }
+                }
+            }
+        }
+    };
+    // This thread's channels of a staged row.
+    auto own = [&](int i, int r, uint32_t shift) {
+        const unsigned char *p = staged_row(i, r) + col * 16;
+        if constexpr (!L::SHIFT) return *reinterpret_cast<const P *>(p);
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(p + (shift & ~3u));
+        uint32_t v[5];
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r)
-                if (base + r < end) store_pack<T, VEC>(s + r * kChannels, v[r]);
+        for (int k = 0; k < 4; ++k) v[k] = w[k];
+        if constexpr (sizeof(T) == 2) {
+            if (shift & 2u) {
+                v[4] = w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = __funnelshift_r(v[k], v[k + 1], 16);
+            }
+        }
+        return *reinterpret_cast<const P *>(v);
+    };
+    // Stores them to their place in memory.
+    auto put = [&](T *p, const P &v) {
+        if constexpr (!L::SHIFT) {
+            store_pack<T, VEC>(p, v);
+        } else if ((reinterpret_cast<uintptr_t>(p) & 3) == 0 && d + VEC <= g.D) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) reinterpret_cast<uint32_t *>(p)[k] = reinterpret_cast<const uint32_t *>(&v)[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k)
+                if (d + k < g.D) p[k] = v.v[k];
         }
     };
     const Walk<const T> wg = walk<const T, BWD>(g.gate, seq, d);
@@ -338,16 +402,16 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
     int base = crank * kStretch + slot * ROWS;  // this thread's first position
     // the next step's gate and x (dh) into buffer pair `i`
     auto stage_next = [&](int at, int i) {
-        stage(wg, at, len, 2 * i);
-        stage(wu, at, len, 2 * i + 1);
+        stage(wg, g.gate, at, copy_len, 2 * i);
+        stage(wu, BWD ? g.dh : g.x, at, copy_len, 2 * i + 1);
     };
     // for the backward pass's second walk: the row before each token (the last
     // position is row 0, whose state before is h0), and x
     auto stage_side = [&](int at) {
         if constexpr (BWD && L::SIDE) {
             const Walk<const T> wh = walk<const T, BWD>(g.h, seq, d);
-            stage({wh.at + wh.step, wh.step}, at, len - 1, 2 * L::STAGES);
-            if constexpr (kSigmoid) stage(walk<const T, BWD>(g.x, seq, d), at, len, 2 * L::STAGES + 1);
+            stage({wh.at + wh.step, wh.step}, g.h, at, copy_len - 1, 2 * L::STAGES);
+            if constexpr (kSigmoid) stage(walk<const T, BWD>(g.x, seq, d), g.x, at, copy_len, 2 * L::STAGES + 1);
         }
     };
     stage_next(base, 0);
@@ -355,7 +419,8 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
     cp_async_commit();
     int parity = 0, i = 0;
     for (; i < steps; ++i, base += step, parity ^= 1) {
-        const T *pg = mine(L::STAGES == 2 ? 2 * parity : 0), *pu = mine(L::STAGES == 2 ? 2 * parity + 1 : 1);
+        const int bg = L::STAGES == 2 ? 2 * parity : 0, bu = bg + 1;  // this step's buffers
+        if constexpr (L::SHIFT) __syncwarp();  // the lanes of a row have read each other's pieces
         P rh[BWD && !L::SIDE ? ROWS : 1], rx[BWD && !L::SIDE && kSigmoid ? ROWS : 1];
         if constexpr (BWD && !L::SIDE) {
             const Walk<const T> wh = walk<const T, BWD>(g.h, seq, d);
@@ -378,6 +443,10 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
         } else {
             cp_async_wait<0>();
         }
+        if constexpr (L::SHIFT) __syncwarp();
+        // the shifts of this thread's rows; the same for the side inputs below
+        const uint32_t shift_g = L::SHIFT ? shift_at(wg, base) - col * 16 : 0, shift_u = L::SHIFT ? shift_at(wu, base) - col * 16 : 0;
+        const uint32_t next_g = (uint32_t)(wg.step * (int64_t)sizeof(T)), next_u = (uint32_t)(wu.step * (int64_t)sizeof(T));
 
         // first walk: (A, H) of the slot
         V a[kKeep ? ROWS : 1][kN], u[kKeep ? ROWS : 1][kN], A[kN], H[kN];
@@ -389,7 +458,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
             if (base + r < len) {
-                const P q = load_pack<T, VEC>(pg + r * kChannels), e = load_pack<T, VEC>(pu + r * kChannels);
+                const P q = own(bg, r, (shift_g + r * next_g) & 15u), e = own(bu, r, (shift_u + r * next_u) & 15u);
 #pragma unroll
                 for (int k = 0; k < kN; ++k) {
                     V at, rest, ut = value(e, k);
@@ -492,8 +561,8 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
                 if (base + r < len) {
                     P o, q, e;
                     if constexpr (!kKeep) {
-                        q = load_pack<T, VEC>(pg + r * kChannels);
-                        e = load_pack<T, VEC>(pu + r * kChannels);
+                        q = own(bg, r, (shift_g + r * next_g) & 15u);
+                        e = own(bu, r, (shift_u + r * next_u) & 15u);
                     }
 #pragma unroll
                     for (int k = 0; k < kN; ++k) {
@@ -504,24 +573,36 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
                         } else {
                             open_gate<T, FORM>(value(q, k), at, rest);
                             ut = value(e, k);
+                            if constexpr (kSigmoid) ut = mul_(ut, rest);
                         }
                         h[k] = mad_(at, h[k], ut);
                         set_value(o, k, h[k]);
                     }
-                    store_pack<T, VEC>(out + r * wo.step, o);
+                    put(out + r * wo.step, o);
                 }
             }
         } else {
             const Walk<T> wo = walk<T, BWD>(g.dgate, seq, d), wx = walk<T, BWD>(g.dx, seq, d);
             T *og = wo.at + base * wo.step, *ox = wx.at + base * wx.step;
+            uint32_t shift_h = 0, shift_x = 0, next_h = 0, next_x = 0;
+            if constexpr (L::SHIFT) {
+                const Walk<const T> wh = walk<const T, BWD>(g.h, seq, d);
+                shift_h = shift_at(wh, base + 1) - col * 16;
+                next_h = (uint32_t)(wh.step * (int64_t)sizeof(T));
+                if constexpr (kSigmoid) {
+                    const Walk<const T> wi = walk<const T, BWD>(g.x, seq, d);
+                    shift_x = shift_at(wi, base) - col * 16;
+                    next_x = (uint32_t)(wi.step * (int64_t)sizeof(T));
+                }
+            }
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
                 if (base + r < len) {
-                    const P q = load_pack<T, VEC>(pg + r * kChannels), e = load_pack<T, VEC>(pu + r * kChannels);
+                    const P q = own(bg, r, (shift_g + r * next_g) & 15u), e = own(bu, r, (shift_u + r * next_u) & 15u);
                     P o0, o1, before, in;
                     if constexpr (L::SIDE) {
-                        before = load_pack<T, VEC>(mine(2 * L::STAGES) + r * kChannels);
-                        if constexpr (kSigmoid) in = load_pack<T, VEC>(mine(2 * L::STAGES + 1) + r * kChannels);
+                        before = own(2 * L::STAGES, r, (shift_h + r * next_h) & 15u);
+                        if constexpr (kSigmoid) in = own(2 * L::STAGES + 1, r, (shift_x + r * next_x) & 15u);
                     } else {
                         before = rh[r];
                         if constexpr (kSigmoid) in = rx[r];
@@ -530,7 +611,8 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
                     Pack<float, VEC> first = {};
                     if (start && g.h0) {
 #pragma unroll
-                        for (int v = 0; v < VEC; ++v) first.v[v] = g.h0[b * g.h0_stride + d + v];
+                        for (int v = 0; v < VEC; ++v)
+                            if (!L::SHIFT || d + v < g.D) first.v[v] = g.h0[b * g.h0_stride + d + v];
                     }
 #pragma unroll
                     for (int k = 0; k < kN; ++k) {
@@ -551,12 +633,13 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
                             set_value(o1, k, mul_(full, rest));
                         }
                     }
-                    store_pack<T, VEC>(og + r * wo.step, o0);
-                    store_pack<T, VEC>(ox + r * wx.step, o1);
+                    put(og + r * wo.step, o0);
+                    put(ox + r * wx.step, o1);
                 }
             }
         }
-        if constexpr (L::STAGES == 1) {  // this thread has read its own places
+        if constexpr (L::SHIFT) __syncwarp();
+        if constexpr (L::STAGES == 1) {  // this thread (SHIFT: row) has been read
             stage_next(base + step, 0);
             if constexpr (L::SIDE) stage_side(base + step);
             cp_async_commit();
@@ -672,8 +755,9 @@ int run(const LinrecArgs &a, cudaStream_t st) {
     bool vec = a.D % kVec == 0 && rows_vec(a, a.gate, sizeof(T)) && rows_vec(a, a.h, sizeof(T));
     if (!BWD || FORM == TRSM_GATE_SIGMOID) vec = vec && rows_vec(a, a.x, sizeof(T));
     if (BWD) vec = vec && rows_vec(a, a.dh, sizeof(T)) && rows_vec(a, a.dgate, sizeof(T)) && rows_vec(a, a.dx, sizeof(T));
-    if (vec) return launch_scan<T, FORM, BWD, Plan<kVec, 8, 256, 32 / kVec, 2, false, 2>>(a, st);
-    return launch_scan<T, FORM, BWD, Plan<1, 32, 256, 8, 2, false, 2>>(a, st);
+    constexpr int kRows = 32 / kVec;
+    if (vec) return launch_scan<T, FORM, BWD, Plan<kVec, 8, 256, kRows, 2, false, false, 2>>(a, st);
+    return launch_scan<T, FORM, BWD, Plan<kVec, 8, 256, kRows, BWD ? 1 : 2, true, true, 2>>(a, st);
 }
 
 template <typename T>

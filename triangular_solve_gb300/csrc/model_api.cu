@@ -65,7 +65,7 @@ int trsm_linrec_forward(trsm_elem_t dtype, trsm_gate_t form, int64_t batch, int6
     if (!good_or_null(h0, 4)) return -12;
     if (!good_or_null(offsets, 4)) return -14;
     if (!empty && !good(h, es)) return -15;
-    if (!offsets && !rows_disjoint(batch, D, h_stride_b)) return -16;
+    if (!offsets && !empty && !rows_disjoint(batch, D, h_stride_b)) return -16;
     if (!rows_disjoint(T, D, h_stride_t)) return -17;
     if (!good_or_null(h_last, 4)) return -18;
     if (empty && !h_last) return TRSM_SUCCESS;
@@ -106,10 +106,10 @@ int trsm_linrec_backward(trsm_elem_t dtype, trsm_gate_t form, int64_t batch, int
     if (!good_or_null(dh_last, 4)) return -20;
     if (!good_or_null(offsets, 4)) return -21;
     if (!empty && !good(dgate, es)) return -22;
-    if (!offsets && !rows_disjoint(batch, D, dgate_stride_b)) return -23;
+    if (!offsets && !empty && !rows_disjoint(batch, D, dgate_stride_b)) return -23;
     if (!rows_disjoint(T, D, dgate_stride_t)) return -24;
     if (!empty && !good(dx, es)) return -25;
-    if (!offsets && !rows_disjoint(batch, D, dx_stride_b)) return -26;
+    if (!offsets && !empty && !rows_disjoint(batch, D, dx_stride_b)) return -26;
     if (!rows_disjoint(T, D, dx_stride_t)) return -27;
     if (!good_or_null(dh0, 4)) return -28;
     if (empty && !dh0) return TRSM_SUCCESS;

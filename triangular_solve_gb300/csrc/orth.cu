@@ -92,9 +92,15 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const Input in, doub
     if (threadIdx.x == 0) partial[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = t;
 }
 
+// Matrices in the workspace lie in panels of 64 columns, each row by row: an
+// operand tile is then one stretch of memory, and one TMA load of several
+// panels.  The last panel is full, with zeros past the last column.
 struct Halves {
     __half *hi, *lo;      // lo: null where X is not split
-    int64_t r, c, ld, stride;
+    int64_t rows, panels;
+    __device__ __forceinline__ int64_t at(int64_t b, int64_t i, int64_t j) const {
+        return ((b * panels + j / 64) * rows + i) * 64 + j % 64;
+    }
 };
 
 // X_0 = 2^14 2^e G in f16 (head and tail), transposed for a tall G, in tiles
@@ -121,9 +127,9 @@ __global__ void __launch_bounds__(256) convert_kernel(const Input in, const doub
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int64_t i = i0 + u + 32 * q, j = j0 + v;
-            if (i >= in.m) continue;
-            float g[8];
-            load_8<T>(G + i * in.ld, j, in.n, in.vec, g);
+            float g[8] = {};
+            if (i < in.m) load_8<T>(G + i * in.ld, j, in.n, in.vec, g);
+            else if (!TALL || out) continue;
             if (out) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -142,24 +148,23 @@ __global__ void __launch_bounds__(256) convert_kernel(const Input in, const doub
                 if (TALL) tile[u + 32 * q][v + k] = g[k];
                 else split(g[k], hi[k], lo[k]);
             }
-            if (!TALL && j < x.ld) {
-                const int64_t at = b * x.stride + i * x.ld + j;
+            if (!TALL) {
+                const int64_t at = x.at(b, i, j);
                 *reinterpret_cast<uint4 *>(x.hi + at) = *reinterpret_cast<const uint4 *>(hi);
                 if (x.lo) *reinterpret_cast<uint4 *>(x.lo + at) = *reinterpret_cast<const uint4 *>(lo);
             }
         }
         if (!TALL || out) continue;
         __syncthreads();
-        // X's row is G's column; rows of the tile past m hold leftovers, which
-        // only reach the padding of X's rows
+        // X's row is G's column
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int64_t i = j0 + u + 32 * q, j = i0 + v;  // of X
-            if (i >= x.r || j >= x.ld) continue;
+            if (i >= x.rows) continue;
             alignas(16) __half hi[8], lo[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) split(tile[v + k][u + 32 * q], hi[k], lo[k]);
-            const int64_t at = b * x.stride + i * x.ld + j;
+            const int64_t at = x.at(b, i, j);
             *reinterpret_cast<uint4 *>(x.hi + at) = *reinterpret_cast<const uint4 *>(hi);
             if (x.lo) *reinterpret_cast<uint4 *>(x.lo + at) = *reinterpret_cast<const uint4 *>(lo);
         }
@@ -169,13 +174,14 @@ __global__ void __launch_bounds__(256) convert_kernel(const Input in, const doub
 // ------------------------------------------------------------------ products
 enum Kind { kGram, kPoly, kApply };  // S = X X^T, C = a I + b S + c S^2, X = C X
 
-// Operands in slabs of 64 along K: a and b (b_lo: the tail's) K-major, 64 x 128
-// and 64 x bn / 2, but X in C X as 64 x 64 with its columns contiguous, and
-// so `above`, S or C from below the diagonal.
+// Operands in slabs of 128 along K, one load each: a and b of 128 and bn / 2
+// rows of two panels; C X's b (b_lo: the tail's), and S S's above the
+// diagonal (`above`), of 128 rows of bn / 128 panels, whose columns are the
+// product's.
 // out, tail: the output in boxes of 32 rows x 64 columns, but a transposed
 // result in boxes of 64 rows x 32 columns.  in: kPoly, S in boxes like out.
 struct Maps {
-    CUtensorMap a, above, b, b_lo, out, tail, in;
+    CUtensorMap a, b, b_lo, above, out, tail, in;
 };
 
 // Tiles of one kind of product, `per` of them a matrix.
@@ -200,11 +206,11 @@ struct Schedule {
     float coef[3 * kMaxSteps];
 };
 
-constexpr int kTileM = 256, kBK = 64;
-constexpr uint32_t kABytes = 128 * kBK * 2;  // 128 rows of A per CTA
-constexpr uint32_t kHalfBytes = 64 * kBK * 2;  // a box of 64 x 64
-constexpr uint32_t kRingBytes = 6 * 2 * kABytes;   // 6 stages of 256-column tiles, 8 of 128-column ones
-constexpr int kMostStages = 8;
+constexpr int kTileM = 256, kBK = 128;
+constexpr uint32_t kABytes = 128 * kBK * 2;     // 128 rows of A per CTA
+constexpr uint32_t kPanelBytes = 128 * 64 * 2;  // 128 rows of a panel
+constexpr uint32_t kRingBytes = 6 * kABytes;    // 3 stages of 256-column tiles, 4 of 128-column ones
+constexpr int kMostStages = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kBox = 32 * 64 * 2;             // bytes of a box of the output
 constexpr int kOutWarps = 8;                       // that empty the accumulators, a box each
@@ -326,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     const uint32_t rank = cluster::rank();
     const bool leader = rank == 0;
     const int pair = (int)blockIdx.x >> 1, npairs = (int)gridDim.x >> 1;
-    const int bn = g.bn, stages = bn == 256 ? 6 : 8;
+    const int bn = g.bn, stages = bn == 256 ? 3 : 4;
     const uint32_t stage_bytes = kRingBytes / stages;
     // The slabs of a tile: `heads` with X's head, as many again with its tail;
     // of each kind, those from `a_above` (`b_above`) on take their part of A
@@ -374,128 +380,114 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         *(volatile int *)&abort_flag = 1;
     };
 
+    // Warps 0 and 1 run as whole warps, with one thread of each issuing: the
+    // addresses and descriptors then stay uniform.
     if (warp == 0) {
-        if (lane == 0) {
-            const uint32_t full0 = cluster::map(full(0), 0);
-            int s = 0, filled = 0;  // the next stage; stages in use the first time round
-            uint32_t phase = 1;     // of empty(s), after the first round
-            for (int t = pair; t < g.tiles && !aborted(); t += npairs) {
-                const Tile x = tile_at(g, t);
-                const Maps &m = maps_of(g, x);
-                if (x.before && !wait_done(g, x.z, x.before)) {
-                    fail();
-                    break;
-                }
-                const int ya = x.tm * kTileM + 128 * (int)rank, yb = x.tn * bn + bn / 2 * (int)rank;
-                const Slabs n = slabs_of(x);
-                const uint32_t bytes = 2 * (kABytes + bn / 2 * kBK * 2);
-                bool ok = true;
-                for (int pass = 0; pass < n.passes && ok; ++pass) {
-                    const CUtensorMap *const columns = x.kind == kPoly ? &m.above : pass ? &m.b_lo : &m.b;
-                    for (int kb = 0; kb < n.heads; ++kb) {
-                        if (filled == stages) {
-                            if (!mbar_wait(empty(s), phase)) {
-                                ok = false;
-                                break;
-                            }
-                        } else {
-                            ++filled;
-                        }
-                        if (leader) mbar_expect_tx(full(s), bytes);
-                        const uint32_t st = base + s * stage_bytes, fb = full0 + 8 * s;
-                        const int kx = kb * kBK;
-                        if (kb < n.a_above) {
-                            tc5::load_pair(st, &m.a, kx, ya, x.z, fb);
-                        } else {
-                            tc5::load_pair(st, &m.above, ya, kx, x.z, fb);
-                            tc5::load_pair(st + kHalfBytes, &m.above, ya + 64, kx, x.z, fb);
-                        }
-                        if (kb < n.b_above) {
-                            tc5::load_pair(st + kABytes, &m.b, kx, yb, x.z, fb);
-                        } else {
-                            tc5::load_pair(st + kABytes, columns, yb, kx, x.z, fb);
-                            if (bn == 256) tc5::load_pair(st + kABytes + kHalfBytes, columns, yb + 64, kx, x.z, fb);
-                        }
-                        if (++s == stages) {
-                            s = 0;
-                            phase ^= 1;
-                        }
+        const uint32_t full0 = cluster::map(full(0), 0);
+        int s = 0, filled = 0;  // the next stage; stages in use the first time round
+        uint32_t phase = 1;     // of empty(s), after the first round
+        bool ok = true;
+        for (int t = pair; t < g.tiles && ok; t += npairs) {
+            const Tile x = tile_at(g, t);
+            const Maps &m = maps_of(g, x);
+            ok = __all_sync(~0u, !x.before || wait_done(g, x.z, x.before));
+            const int ya = x.tm * kTileM + 128 * (int)rank, yb = x.tn * bn + bn / 2 * (int)rank;
+            const Slabs n = slabs_of(x);
+            for (int pass = 0; pass < n.passes && ok; ++pass) {
+                const CUtensorMap *const columns = x.kind == kPoly ? &m.above : pass ? &m.b_lo : &m.b;
+                for (int kb = 0; kb < n.heads; ++kb) {
+                    if (filled == stages) {
+                        ok = __all_sync(~0u, mbar_wait(empty(s), phase));
+                        if (!ok) break;
+                    } else {
+                        ++filled;
                     }
-                }
-                if (!ok) {
-                    fail();
-                    break;
-                }
-            }
-            if (aborted() && leader) {
-                // the pair's loads counted on these barriers land before shared
-                // memory goes away: the newest of each stage in use
-                for (int j = 0; j < filled; ++j) {
-                    s = s ? s - 1 : stages - 1;
-                    if (s == stages - 1) phase ^= 1;
-                    if (!mbar_wait(full(s), phase ^ 1)) record_timeout(g.status);
+                    const uint32_t st = base + s * stage_bytes, fb = full0 + 8 * s;
+                    if (tc5::elect()) {
+                        if (leader) mbar_expect_tx(full(s), 2 * stage_bytes);
+                        if (kb < n.a_above) tc5::load_pair(st, &m.a, 0, ya, 2 * kb, x.z, fb);
+                        else tc5::load_pair(st, &m.a, 0, kb * kBK, ya / 64, x.z, fb);
+                        if (kb < n.b_above) tc5::load_pair(st + kABytes, &m.b, 0, yb, 2 * kb, x.z, fb);
+                        else tc5::load_pair(st + kABytes, columns, 0, kb * kBK, yb / 64, x.z, fb);
+                    }
+                    if (++s == stages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
             }
         }
+        if (!ok && lane == 0) fail();
+        __syncwarp();
+        if (aborted() && leader && lane == 0) {
+            // the pair's loads counted on these barriers land before shared
+            // memory goes away: the newest of each stage in use
+            for (int j = 0; j < filled; ++j) {
+                s = s ? s - 1 : stages - 1;
+                if (s == stages - 1) phase ^= 1;
+                if (!mbar_wait(full(s), phase ^ 1)) record_timeout(g.status);
+            }
+        }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
             int i = 0, s = 0;
             uint32_t phase = 0;  // of full(s)
-            for (int t = pair; t < g.tiles && !aborted(); t += npairs, ++i) {
+            bool ok = true;
+            for (int t = pair; t < g.tiles && ok; t += npairs, ++i) {
                 const Tile x = tile_at(g, t);
                 const int a = i & 1;
                 const Slabs n = slabs_of(x);
-                if (i >= 2 && !mbar_wait(acc_empty(a), ((i >> 1) - 1) & 1)) {
-                    fail();
-                    break;
-                }
+                ok = __all_sync(~0u, i < 2 || mbar_wait(acc_empty(a), ((i >> 1) - 1) & 1));
                 tc5::fence_after();
                 const uint32_t d = tmem + (uint32_t)(a * 256);
-                bool ok = true;
                 uint32_t accumulate = 0;
                 // slabs kb .. end - 1, all with their operands the same way round
                 auto run = [&](int kb, int end, bool a_mn, bool b_mn) {
-                    // 16 of K are 32 bytes on in a row, 16 rows of 128 bytes otherwise
-                    const uint64_t da0 = a_mn ? tc5::desc_mn_major(base, kHalfBytes) : tc5::desc_k_major(base);
+                    const uint64_t da0 = a_mn ? tc5::desc_mn_major(base, kPanelBytes) : tc5::desc_k_major(base);
                     const uint64_t db0 =
-                        b_mn ? tc5::desc_mn_major(base + kABytes, kHalfBytes) : tc5::desc_k_major(base + kABytes);
-                    const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
+                        b_mn ? tc5::desc_mn_major(base + kABytes, kPanelBytes) : tc5::desc_k_major(base + kABytes);
+                    // 16 of K are 32 bytes on in a row and 64 the next panel, or 16 rows of 128 bytes
+                    const uint32_t sa = (a_mn ? 2048 : 32) >> 4, sb = (b_mn ? 2048 : 32) >> 4;
+                    const uint32_t pa = (a_mn ? 4 * 2048 : kPanelBytes) >> 4;
+                    const uint32_t pb = (b_mn ? 4 * 2048 : (uint32_t)bn / 2 * 128) >> 4;
                     const uint32_t idesc = tc5::idesc_f16(kTileM, bn, a_mn, b_mn);
                     for (; kb < end && ok; ++kb) {
                         bool come = mbar_wait(full(s), phase);
                         // the loader may itself be waiting for an earlier product
-                        for (int tries = 1; tries < kPatience && !come && !aborted(); ++tries)
-                            come = mbar_wait(full(s), phase);
-                        if (!come) {
-                            fail();
-                            ok = false;
-                            break;
-                        }
+                        for (int tries = 1; tries < kPatience && !come; ++tries)
+                            come = !aborted() && mbar_wait(full(s), phase);
+                        ok = __all_sync(~0u, come);
+                        if (!ok) break;
                         tc5::fence_after();
                         const uint64_t da = da0 + s * (stage_bytes >> 4), db = db0 + s * (stage_bytes >> 4);
+                        if (tc5::elect()) {
 #pragma unroll
-                        for (int kk = 0; kk < kBK / 16; ++kk) {
-                            tc5::mma_pair(d, da + kk * sa, db + kk * sb, idesc, accumulate);
-                            accumulate = 1;
+                            for (int kk = 0; kk < kBK / 16; ++kk)
+                                tc5::mma_pair(d, da + (kk & 3) * sa + (kk >> 2) * pa, db + (kk & 3) * sb + (kk >> 2) * pb,
+                                              idesc, kk ? 1 : accumulate);
+                            tc5::commit_both(empty(s));  // both CTAs' slab is free once these have read it
                         }
-                        tc5::commit_both(empty(s));  // both CTAs' slab is free once these have read it
+                        accumulate = 1;
                         if (++s == stages) {
                             s = 0;
                             phase ^= 1;
                         }
                     }
                 };
-                for (int pass = 0; pass < n.passes; ++pass) {
-                    const int first = min(n.a_above, n.b_above), second = max(n.a_above, n.b_above);
-                    run(0, first, false, false);
-                    run(first, second, n.a_above <= first, n.b_above <= first);
-                    run(second, n.heads, true, true);
+                if (ok) {
+                    for (int pass = 0; pass < n.passes; ++pass) {
+                        const int first = min(n.a_above, n.b_above), second = max(n.a_above, n.b_above);
+                        run(0, first, false, false);
+                        run(first, second, n.a_above <= first, n.b_above <= first);
+                        run(second, n.heads, true, true);
+                    }
                 }
-                tc5::commit_both(acc_full(a));
-                if (!ok) break;
+                if (tc5::elect()) tc5::commit_both(acc_full(a));
             }
-            tc5::commit_local(drain);
-            if (!mbar_wait(drain, 0)) record_timeout(g.status);
+            if (!ok && lane == 0) fail();
+            __syncwarp();
+            if (tc5::elect()) tc5::commit_local(drain);
+            if (!mbar_wait(drain, 0) && lane == 0) record_timeout(g.status);
         }
     } else if (warp == 2 + kOutWarps) {
         if (lane == 0) {
@@ -540,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                                                 : rho / kScaleS / (finish ? kScaleX : 1.f);
             auto fetch_s = [&](int q) {  // lane 0: S's box of group q, into this warp's
                 mbar_expect_tx(s_full(me), kBox);
-                tma_load_3d(base + box, &maps.in, col0 + 64 * q, row0, z, s_full(me));
+                tc5::load_4d(base + box, &maps.in, 0, row0, col0 / 64 + q, z, s_full(me));
             };
             bool come = true;
             if (poly && group0 < groups && lane == 0) {
@@ -655,7 +647,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                 __syncwarp();
                 if (lane == 0) {
                     if (turned) tma_store_3d(&maps.out, row0, col, z, base + box);
-                    else tma_store_3d(&maps.out, col, row0, z, base + box);
+                    else if (finish) tma_store_3d(&maps.out, col, row0, z, base + box);
+                    else tc5::store_4d(&maps.out, 0, row0, col / 64, z, base + box);
                     bulk_commit();
                 }
                 if (tail) {
@@ -668,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_3d(&maps.tail, col, row0, z, base + box);
+                        tc5::store_4d(&maps.tail, 0, row0, col / 64, z, base + box);
                         bulk_commit();
                     }
                 }
@@ -694,8 +687,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 }
 
 // ------------------------------------------------------------------ launch
-int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
-
 // Which X_k (k = 0 .. steps - 1) have a tail: those whose rounding the steps
 // from k on can amplify more than kMostAmplified times.  X_0 of a 16-bit
 // input is exact.
@@ -716,15 +707,15 @@ int norm_blocks(int64_t m, int64_t n) {
 // reads one and writes the other), its tails twice, S, C, the partial sums,
 // rho and the counters of finished tiles.
 struct Layout {
-    int64_t r, c, ldx, lds;
+    int64_t r, c, xp, sp;  // panels of X, and of S and C
     size_t x, s, partial, rho, done;
     Layout(int64_t m, int64_t n, int64_t batch) {
         r = m < n ? m : n;
         c = m < n ? n : m;
-        ldx = up8(c);
-        lds = up8(r);
-        x = (size_t)round256(batch * r * ldx * 2);
-        s = (size_t)round256(batch * r * lds * 2);
+        xp = (c + 63) / 64;
+        sp = (r + 63) / 64;
+        x = (size_t)round256(batch * r * xp * 128);
+        s = (size_t)round256(batch * r * sp * 128);
         partial = (size_t)round256(batch * norm_blocks(m, n) * 8);
         rho = (size_t)round256(batch * 4);
         done = (size_t)round256((batch + 1) * 4);
@@ -732,13 +723,9 @@ struct Layout {
     size_t total() const { return 4 * x + 2 * s + partial + rho + done; }
 };
 
-// An f16 (or 16-bit) matrix per batch entry, inner x rows; ld and stride in elements.
-struct Matrix {
-    const void *p;
-    int64_t inner, rows, ld, stride;
-};
-
-int make_map(CUtensorMap *map, const Matrix &x, int64_t batch, int box_inner, int box_rows, bool swizzled = true) {
+using Dims = cuuint64_t[4];
+int make_map(CUtensorMap *map, const void *p, const Dims &dims, const cuuint64_t *strides, const cuuint32_t *box, int rank,
+             bool swizzled) {
     static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -748,14 +735,28 @@ int make_map(CUtensorMap *map, const Matrix &x, int64_t batch, int box_inner, in
         return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }();
     if (!encode) return TRSM_ERR_CUDA_BASE + (int)cudaErrorNotSupported;
-    const cuuint64_t dims[3] = {(cuuint64_t)x.inner, (cuuint64_t)x.rows, (cuuint64_t)batch};
-    const cuuint64_t strides[2] = {(cuuint64_t)(x.ld * 2), (cuuint64_t)(x.stride * 2)};
-    const cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, 1}, one[3] = {1, 1, 1};
-    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(x.p), dims, strides, box, one,
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void *>(p), dims, strides, box, one,
                               CU_TENSOR_MAP_INTERLEAVE_NONE,
                               swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? TRSM_SUCCESS : TRSM_ERR_CUDA_BASE + (int)cudaErrorInvalidValue;
+}
+// Boxes of `panels` panels x `box_rows` rows of matrices in panels.
+int panel_map(CUtensorMap *map, const void *p, int64_t rows, int64_t panels, int64_t batch, int box_rows,
+              int box_panels) {
+    const Dims dims = {64, (cuuint64_t)rows, (cuuint64_t)panels, (cuuint64_t)batch};
+    const cuuint64_t strides[3] = {128, (cuuint64_t)rows * 128, (cuuint64_t)(rows * panels) * 128};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_panels, 1};
+    return make_map(map, p, dims, strides, box, 4, true);
+}
+// The same of row-major m x n matrices of 16-bit elements (the result).
+int row_map(CUtensorMap *map, const void *p, int64_t m, int64_t n, int64_t batch, int64_t ld, int64_t stride, int box_rows,
+            int box_cols, bool swizzled) {
+    const Dims dims = {(cuuint64_t)n, (cuuint64_t)m, (cuuint64_t)batch, 0};
+    const cuuint64_t strides[2] = {(cuuint64_t)(ld * 2), (cuuint64_t)(stride * 2)};
+    const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+    return make_map(map, p, dims, strides, box, 3, swizzled);
 }
 
 // CTA pairs that run at once, one CTA an SM.
@@ -801,26 +802,20 @@ Tiling tiling(int64_t r, int64_t N, bool symmetric, int bn) {
     return t;
 }
 
-// Columns of a tile, 256 or 128: whichever takes less time by the time of a
-// slab of K (0.31 us of a 256 x 256 tile, 0.20 of a 256 x 128 one) and of a
-// product's way out (3 and 2 us).  One matrix's product takes whole rounds of
-// the CTA pairs; those of several run into each other.
+// Columns of a tile, 256 or 128: whichever takes less time by that of 64 of K
+// (0.31 us of a 256 x 256 tile, 0.19 of a 256 x 128 one) and of a tile's way
+// out.  One matrix's product takes whole rounds of the CTA pairs; those of
+// several run into each other.
 int choose_bn(int64_t r, int64_t c, int64_t batch, int pairs) {
-    double least = 0;
-    int best = 256;
-    for (int bn = 256; bn >= 128; bn /= 2) {
+    auto cost = [&](int bn) {
         auto rounds = [&](const Tiling &t) {
             const double n = (double)t.per * batch / pairs;
             return n < 1 ? 1.0 : batch == 1 ? ceil(n) : n;
         };
         const double sym = rounds(tiling(r, r, true, bn)), app = rounds(tiling(r, c, false, bn));
-        const double cost = (bn == 256 ? 0.31 : 0.20) / kBK * (sym * (c + r) + app * r) + (bn == 256 ? 9 : 6);
-        if (bn == 256 || cost < least) {
-            best = bn;
-            least = cost;
-        }
-    }
-    return best;
+        return (bn == 256 ? 0.31 : 0.19) / 64 * (sym * (c + r) + app * r) + (bn == 256 ? 3 * 4.5 : 3 * 3.5);
+    };
+    return cost(256) <= cost(128) ? 256 : 128;
 }
 
 template <typename T>
@@ -859,7 +854,7 @@ int run(const OrthArgs &a, unsigned long long tails, cudaStream_t st) {
     const int64_t es = a.in_dtype == TRSM_ELEM_F32 ? 4 : 2;
     Input in = {a.G, a.m, a.n, a.ldg, a.strideG, false};
     in.vec = rows_on_16_bytes(a.G, a.m, a.ldg, a.batch, a.strideG, es);
-    const Halves x0 = {xh[0], tails & 1 ? xl[0] : nullptr, w.r, w.c, w.ldx, w.r * w.ldx};
+    const Halves x0 = {xh[0], tails & 1 ? xl[0] : nullptr, w.r, w.xp};
     int rc;
     switch (a.in_dtype) {
         case TRSM_ELEM_F32: rc = convert<float>(a, in, x0, partial, rho, done, st); break;
@@ -890,34 +885,33 @@ int run(const OrthArgs &a, unsigned long long tails, cudaStream_t st) {
 
     // every tensor map that the steps use: each buffer in each part that it
     // plays, by turns for X
-    const Matrix mS = {S, w.r, w.r, w.lds, w.r * w.lds}, mC = {C, w.r, w.r, w.lds, w.r * w.lds};
     Maps *const gram = g.gram, *const apply = g.apply, &poly = g.poly;
-    auto map = [&](CUtensorMap *m, const Matrix &x, int inner, int rows, bool swizzled = true) {
-        if (!rc) rc = make_map(m, x, a.batch, inner, rows, swizzled);
+    auto x_map = [&](CUtensorMap *m, const __half *p, int rows, int panels) {
+        if (!rc) rc = panel_map(m, p, w.r, w.xp, a.batch, rows, panels);
+    };
+    auto s_map = [&](CUtensorMap *m, const __half *p, int rows, int panels) {
+        if (!rc) rc = panel_map(m, p, w.r, w.sp, a.batch, rows, panels);
     };
     for (int k = 0; k < 2; ++k) {
-        const Matrix mX = {xh[k], w.c, w.r, w.ldx, w.r * w.ldx}, mL = {xl[k], w.c, w.r, w.ldx, w.r * w.ldx};
         if (k && a.steps == 1) break;
         // S = X X^T
-        map(&gram[k].a, mX, kBK, 128);
-        map(&gram[k].b, mX, kBK, g.bn / 2);
-        if (k == 0) map(&gram[0].out, mS, 64, 32);
+        x_map(&gram[k].a, xh[k], 128, 2);
+        x_map(&gram[k].b, xh[k], g.bn / 2, 2);
+        if (k == 0) s_map(&gram[0].out, S, 32, 1);
         else gram[1].out = gram[0].out;
         // X = C X, from buffer k to the other
-        map(&apply[k].b, mX, 64, kBK);
-        map(&apply[k].b_lo, mL, 64, kBK);
-        map(&apply[k ^ 1].out, mX, 64, 32);
-        map(&apply[k ^ 1].tail, mL, 64, 32);
+        x_map(&apply[k].b, xh[k], 128, g.bn / 128);
+        x_map(&apply[k].b_lo, xl[k], 128, g.bn / 128);
+        x_map(&apply[k ^ 1].out, xh[k], 32, 1);
+        x_map(&apply[k ^ 1].tail, xl[k], 32, 1);
     }
-    map(&poly.a, mS, kBK, 128);
-    map(&poly.above, mS, 64, kBK);
-    map(&poly.b, mS, kBK, g.bn / 2);
-    map(&poly.out, mC, 64, 32);
+    s_map(&poly.a, S, 128, 2);
+    s_map(&poly.b, S, g.bn / 2, 2);
+    s_map(&poly.above, S, 128, g.bn / 128);
+    s_map(&poly.out, C, 32, 1);
     poly.in = gram[0].out;
-    map(&apply[0].a, mC, kBK, 128);
-    map(&apply[0].above, mC, 64, kBK);
+    s_map(&apply[0].a, C, 128, 2);
     apply[1].a = apply[0].a;
-    apply[1].above = apply[0].above;
     // the last product writes O, by TMA where its rows start on 16-byte boundaries
     Maps &finish = g.finish;
     finish = apply[(a.steps - 1) & 1];
@@ -925,11 +919,9 @@ int run(const OrthArgs &a, unsigned long long tails, cudaStream_t st) {
     const bool direct = !rows_on_16_bytes(a.O, a.m, a.ldo, a.batch, a.strideO, 2);
     if (!direct) {
         // strides of a single row or matrix are of no account, but a map needs valid ones
-        const int64_t ld = a.m > 1 ? a.ldo : up8(a.n), so = a.batch > 1 ? a.strideO : up8(a.m * ld);
-        const Matrix mO = {a.O, a.n, a.m, ld, so};
-        map(&finish.out, mO, tall ? 32 : 64, tall ? 64 : 32, !tall);
+        const int64_t ld = a.m > 1 ? a.ldo : (a.n + 7) / 8 * 8, so = a.batch > 1 ? a.strideO : (a.m * ld + 7) / 8 * 8;
+        if (!rc) rc = row_map(&finish.out, a.O, a.m, a.n, a.batch, ld, so, tall ? 64 : 32, tall ? 32 : 64, !tall);
     }
-
     if (rc) return rc;
     g.transposed = tall;
     g.bf16 = a.out_dtype == TRSM_ELEM_BF16;

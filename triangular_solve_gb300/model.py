@@ -122,83 +122,81 @@ def _load_torch():
     return _torch
 
 
-def _on_device(t, launch):
-    """Runs launch(stream) with t's device current, on its current stream."""
-    cuda = _torch.cuda
-    if t.get_device() == cuda.current_device():
-        return launch(cuda.current_stream().cuda_stream)
-    with cuda.device(t.device):
-        return launch(cuda.current_stream().cuda_stream)
+def _launch(fn, dev, *args):
+    """Calls entry point `fn` with device `dev` current, on its current stream."""
+    cuda = _torch._C
+    if dev == cuda._cuda_getDevice():
+        return fn(*args, cuda._cuda_getCurrentRawStream(dev))
+    with _torch.cuda.device(dev):
+        return fn(*args, cuda._cuda_getCurrentRawStream(dev))
 
 
-def _rows(name, t, like):
-    """A tensor of `like`'s shape, type and device with contiguous channels."""
-    if t.shape != like.shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(like.shape)}")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name}: {t.dtype}, expected {like.dtype}")
-    if t.get_device() != like.get_device():
-        raise ValueError(f"{name}: on {t.device}, expected {like.device}")
+def _refuse(name, t, shape, dtype, dev):
+    """Says what is wrong with a tensor that is not one of `shape`, `dtype` and
+    device `dev` with contiguous channels; returns where nothing is."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
     if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
         raise ValueError(f"{name}: the channels (last dimension) must be contiguous")
 
 
-def _float_state(name, t, shape, like):
-    if t.dtype != _torch.float32:
-        raise TypeError(f"{name}: states are float32, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    if t.get_device() != like.get_device():
-        raise ValueError(f"{name}: on {t.device}, expected {like.device}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
-        raise ValueError(f"{name}: the channels (last dimension) must be contiguous")
+def _rows(name, t, shape, dtype, dev):
+    """Pointer and strides (batch, token) of a tensor like the gate."""
+    st = t.stride()
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or st[-1] != 1:
+        _refuse(name, t, shape, dtype, dev)
+    return (t.data_ptr(), st[0], st[1]) if len(st) == 3 else (t.data_ptr(), 0, st[0])
 
 
-def _geometry(gate, offsets):
-    """(element code, batch, T, D) of batched or packed sequences."""
-    if not gate.is_cuda:
-        raise ValueError("the recurrence takes CUDA (device) tensors; got a CPU tensor")
+def _state(name, t, shape, dev):
+    """Pointer and row stride of float32 states."""
+    if t is None:
+        return None, 0
+    st = t.stride()
+    if t.dtype is not _torch.float32 or t.shape != shape or t.get_device() != dev or st[-1] != 1:
+        _refuse(name, t, shape, _torch.float32, dev)
+    return t.data_ptr(), st[0]
+
+
+def _gate(gate, offsets):
+    """(element code, form-independent geometry) of the gate: code, batch, T, D,
+    device and the offsets' pointer."""
     code = _elem.get(gate.dtype)
+    dev = gate.get_device()
+    if dev < 0:
+        raise ValueError("gate: the recurrence takes CUDA (device) tensors; got a CPU tensor")
     if code is None:
         raise TypeError(f"gate: {gate.dtype} (float32, float16 or bfloat16)")
-    if gate.stride(-1) != 1 and gate.shape[-1] > 1 and gate.numel():
-        raise ValueError("gate: the channels (last dimension) must be contiguous")
+    shape = gate.shape
     if offsets is None:
-        if gate.dim() != 3:
+        if len(shape) != 3:
             raise ValueError("gate: expected (batch, T, D), or (rows, D) with offsets")
-        return code, gate.shape[0], gate.shape[1], gate.shape[2]
-    if gate.dim() != 2:
+        return code, shape[0], shape[1], shape[2], dev, None
+    if len(shape) != 2:
         raise ValueError("gate: packed sequences (offsets) are (rows, D)")
-    if offsets.dtype != _torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_contiguous():
+    if offsets.dtype is not _torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_contiguous():
         raise ValueError("offsets: a contiguous int32 vector of batch + 1 row numbers")
-    if offsets.get_device() != gate.get_device():
+    if offsets.get_device() != dev:
         raise ValueError(f"offsets: on {offsets.device}, expected {gate.device}")
-    return code, offsets.shape[0] - 1, gate.shape[0], gate.shape[1]
-
-
-def _strides(t):
-    """(pointer, stride_b, stride_t) of a batched or packed tensor."""
-    if t.dim() == 3:
-        return t.data_ptr(), t.stride(0), t.stride(1)
-    return t.data_ptr(), 0, t.stride(0)
-
-
-def _pointer(t):
-    return None if t is None else t.data_ptr()
+    return code, offsets.shape[0] - 1, shape[0], shape[1], dev, offsets.data_ptr()
 
 
 def _forward(gate, x, h0, form, offsets):
     torch = _load_torch()
-    code, batch, T, D = _geometry(gate, offsets)
+    code, batch, T, D, dev, po = _gate(gate, offsets)
     kind = _code(FORMS, form, "form")
-    _rows("x", x, gate)
-    if h0 is not None:
-        _float_state("h0", h0, (batch, D), gate)
-    h = torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
+    shape, dtype = gate.shape, gate.dtype
+    pg, px, ps = _rows("gate", gate, shape, dtype, dev), _rows("x", x, shape, dtype, dev), _state("h0", h0, (batch, D), dev)
+    h = torch.empty(shape, dtype=dtype, device=gate.device)
     last = torch.empty((batch, D), dtype=torch.float32, device=gate.device)
-    _check("trsm_linrec_forward", _on_device(gate, lambda st: _library().trsm_linrec_forward(
-        code, kind, batch, T, D, *_strides(gate), *_strides(x), _pointer(h0), 0 if h0 is None else h0.stride(0),
-        _pointer(offsets), *_strides(h), last.data_ptr(), st)))
+    status = _launch(_library().trsm_linrec_forward, dev, code, kind, batch, T, D, *pg, *px, *ps, po, h.data_ptr(),
+                     T * D, D, last.data_ptr())
+    if status:
+        _check("trsm_linrec_forward", status)
     return h, last
 
 
@@ -207,27 +205,28 @@ def linear_recurrence_backward(gate, x, h, dh, h0=None, dh_last=None, *, form="d
     output, and ``dh`` and ``dh_last``, the gradients of its two results
     (dh_last None: zero).  ``x`` may be None unless form is "sigmoid"."""
     torch = _load_torch()
-    code, batch, T, D = _geometry(gate, offsets)
+    code, batch, T, D, dev, po = _gate(gate, offsets)
     kind = _code(FORMS, form, "form")
+    shape, dtype = gate.shape, gate.dtype
+    pg, ph, pd = (_rows(name, t, shape, dtype, dev) for name, t in (("gate", gate), ("h", h), ("dh", dh)))
     if x is not None:
-        _rows("x", x, gate)
+        px = _rows("x", x, shape, dtype, dev)
     elif kind == FORMS["sigmoid"]:
         raise ValueError("x: needed by the sigmoid form")
-    _rows("h", h, gate)
-    _rows("dh", dh, gate)
-    if h0 is not None:
-        _float_state("h0", h0, (batch, D), gate)
-    if dh_last is not None:
-        _float_state("dh_last", dh_last, (batch, D), gate)
-        if not dh_last.is_contiguous():
-            dh_last = dh_last.contiguous()
-    dgate = torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
-    dx = torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
+    else:
+        px = (None, 0, 0)
+    ps = _state("h0", h0, (batch, D), dev)
+    pl, ld = _state("dh_last", dh_last, (batch, D), dev)
+    if pl and ld != D and batch > 1:
+        dh_last = dh_last.contiguous()
+        pl = dh_last.data_ptr()
+    dgate = torch.empty(shape, dtype=dtype, device=gate.device)
+    dx = torch.empty(shape, dtype=dtype, device=gate.device)
     dh0 = torch.empty((batch, D), dtype=torch.float32, device=gate.device)
-    _check("trsm_linrec_backward", _on_device(gate, lambda st: _library().trsm_linrec_backward(
-        code, kind, batch, T, D, *_strides(gate), *((None, 0, 0) if x is None else _strides(x)), *_strides(h),
-        _pointer(h0), 0 if h0 is None else h0.stride(0), *_strides(dh), _pointer(dh_last), _pointer(offsets),
-        *_strides(dgate), *_strides(dx), dh0.data_ptr(), st)))
+    status = _launch(_library().trsm_linrec_backward, dev, code, kind, batch, T, D, *pg, *px, *ph, *ps, *pd, pl, po,
+                     dgate.data_ptr(), T * D, D, dx.data_ptr(), T * D, D, dh0.data_ptr())
+    if status:
+        _check("trsm_linrec_backward", status)
     return dgate, dx, dh0
 
 
@@ -283,8 +282,8 @@ def linear_recurrence(gate, x, h0=None, *, form="decay", offsets=None):
     Returns (h, h_last): all states, of gate's type, and the last ones in
     float32.  Differentiable in gate, x and h0.
     """
-    torch = _load_torch()
-    if torch.is_grad_enabled() and (gate.requires_grad or x.requires_grad or (h0 is not None and h0.requires_grad)):
+    if (gate.requires_grad or x.requires_grad or (h0 is not None and h0.requires_grad)) and \
+            _load_torch().is_grad_enabled():
         return _autograd().apply(gate, x, h0, form, offsets)
     return _forward(gate, x, h0, form, offsets)
 
@@ -298,34 +297,35 @@ def linear_recurrence_step(gate, x, state, *, form="decay", slots=None, out_stat
     padding: zero comes out and no state is touched.  Returns the new states
     as (batch, D) of gate's type."""
     torch = _load_torch()
-    if not gate.is_cuda:
-        raise ValueError("the recurrence takes CUDA (device) tensors; got a CPU tensor")
-    code = _elem.get(gate.dtype)
+    shape, dtype, dev = gate.shape, gate.dtype, gate.get_device()
+    code = _elem.get(dtype)
+    if dev < 0:
+        raise ValueError("gate: the recurrence takes CUDA (device) tensors; got a CPU tensor")
     if code is None:
-        raise TypeError(f"gate: {gate.dtype} (float32, float16 or bfloat16)")
-    if gate.dim() != 2:
+        raise TypeError(f"gate: {dtype} (float32, float16 or bfloat16)")
+    if len(shape) != 2:
         raise ValueError("gate: expected (batch, D)")
     kind = _code(FORMS, form, "form")
-    batch, D = gate.shape
-    _rows("gate", gate, gate)
-    _rows("x", x, gate)
+    batch, D = shape
+    pg, _, sg = _rows("gate", gate, shape, dtype, dev)
+    px, _, sx = _rows("x", x, shape, dtype, dev)
     if state.dim() != 2:
         raise ValueError("state: expected (slots, D)")
-    _float_state("state", state, (state.shape[0], D), gate)
-    if out_state is None:
-        out_state = state
-    else:
-        _float_state("out_state", out_state, (state.shape[0], D), gate)
+    table = (state.shape[0], D)
+    ps, ss = _state("state", state, table, dev)
+    pn, sn = (ps, ss) if out_state is None else _state("out_state", out_state, table, dev)
+    pi = None
     if slots is not None:
-        if slots.dtype != torch.int32 or slots.shape != (batch,) or (batch > 1 and slots.stride(0) != 1):
+        if slots.dtype is not torch.int32 or slots.shape != (batch,) or (batch > 1 and slots.stride(0) != 1):
             raise ValueError("slots: a contiguous int32 vector of batch state numbers")
-        if slots.get_device() != gate.get_device():
+        if slots.get_device() != dev:
             raise ValueError(f"slots: on {slots.device}, expected {gate.device}")
-    y = torch.empty((batch, D), dtype=gate.dtype, device=gate.device)
-    _check("trsm_linrec_step", _on_device(gate, lambda st: _library().trsm_linrec_step(
-        code, kind, batch, D, gate.data_ptr(), gate.stride(0), x.data_ptr(), x.stride(0), _pointer(slots),
-        state.shape[0], state.data_ptr(), state.stride(0), out_state.data_ptr(), out_state.stride(0), y.data_ptr(), D,
-        st)))
+        pi = slots.data_ptr()
+    y = torch.empty(shape, dtype=dtype, device=gate.device)
+    status = _launch(_library().trsm_linrec_step, dev, code, kind, batch, D, pg, sg, px, sx, pi, table[0], ps, ss, pn, sn,
+                     y.data_ptr(), D)
+    if status:
+        _check("trsm_linrec_step", status)
     return y
 
 
@@ -391,7 +391,8 @@ def orthogonalize(G, *, steps=5, coefficients=None, eps=1e-7, out=None):
     if flip:
         m, n = n, m
     batch = G.shape[0] if G.dim() == 3 else 1
-    _check("trsm_orthogonalize", _on_device(G, lambda st: _library().trsm_orthogonalize(
-        code, _elem[out.dtype], m, n, G.data_ptr(), ldg, sg, out.data_ptr(), ldo, so, batch, steps, coef, eps, None, 0,
-        st)))
+    status = _launch(_library().trsm_orthogonalize, G.get_device(), code, _elem[out.dtype], m, n, G.data_ptr(), ldg, sg,
+                     out.data_ptr(), ldo, so, batch, steps, coef, eps, None, 0)
+    if status:
+        _check("trsm_orthogonalize", status)
     return out
