@@ -170,8 +170,8 @@ def test_batched_forward_and_backward(env, name, form, shape):
 
 @pytest.mark.parametrize("name", ["f32", "bf16"])
 @pytest.mark.parametrize("form", ["decay", "sigmoid"])
-@pytest.mark.parametrize("lengths", [[0], [1], [0, 0, 3], [5, 0, 1, 1, 130, 0], [257, 1, 1024, 64], [3, 2000, 2]],
-                         ids=str)
+@pytest.mark.parametrize("lengths", [[0], [1], [0, 0, 3], [5, 0, 1, 1, 130, 0], [257, 1, 1024, 64], [3, 2000, 2],
+                                     [7] * 45 + [600, 0] + [2] * 30 + [513, 1500, 1]], ids=str)
 @pytest.mark.parametrize("D", [40, 61])
 def test_packed_sequences(env, name, form, lengths, D):
     torch, tg = env

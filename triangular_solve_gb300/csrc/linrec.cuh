@@ -16,8 +16,8 @@
 // (forward 3 elements a token and channel, backward 5, or 6 in the sigmoid
 // form) and does a few operations on each.
 //
-// Layout.  A CTA of 256 threads takes 16 bytes of channels per lane and 8
-// lanes side by side, and 32 time slots of ROWS consecutive tokens each.
+// Layout.  A CTA takes 16 bytes of channels per lane and 2 to 8 lanes side by
+// side, and as many time slots of ROWS consecutive tokens as its threads make.
 // Every thread copies its own tokens into shared memory ahead of time
 // (cp.async, so no registers and no block barrier are spent on it) and walks
 // them twice from there; they are read from memory once.  Rows that do not
@@ -45,6 +45,7 @@ namespace trsm {
 namespace linrec {
 
 constexpr int kMaxCluster = 8;
+constexpr int kLong = 2;  // stretches of a CTA; a packed sequence above takes a cluster
 
 template <typename T> __device__ __forceinline__ float to_f32(T v);
 template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
@@ -261,7 +262,9 @@ template <int VEC_, int LANES_, int THREADS, int ROWS_, int STAGES_, bool SIDE_,
     }
 };
 
-template <typename T, int FORM, bool BWD, typename L>
+// PACKED: packed sequences (a kernel of its own, since its loop over sequences
+// costs the batched one 7%).
+template <typename T, int FORM, bool BWD, bool PACKED, typename L>
 __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
     scan_kernel(const __grid_constant__ LinrecArgs g, const int groups) {
     constexpr int VEC = L::VEC, LANES = L::LANES, ROWS = L::ROWS;
@@ -286,34 +289,15 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
     const int tid = threadIdx.x, col = tid % LANES, slot = tid / LANES;
     // Between the walks thread (place, part) composes the slots of one part.
     const int place = tid % kChannels, part = tid / kChannels;
-    const int csize = (int)cluster::size(), crank = (int)cluster::rank();
-    const int64_t unit = (int64_t)(blockIdx.x / csize);
-    const int64_t b = unit / groups;
-    const int64_t c0 = (unit % groups) * kChannels;
-    const int64_t d = c0 + col * VEC;
-    const bool live = d < g.D;
-    const Sequence seq = sequence(g, b);
-    const int len = live ? seq.len : 0;  // tokens that this thread walks
-    // and copies: a piece may hold channels of the lane before only
-    const int copy_len = L::SHIFT ? seq.len : len;
-
-    // each of them carries the state of its channel from step to step
-    const int64_t dc = c0 + L::channel_at(place);
-    float carry = 0.f;
-    if (dc < g.D) {
-        if constexpr (BWD) {
-            if (g.dh_last) carry = g.dh_last[b * g.D + dc];
-        } else {
-            if (g.h0) carry = g.h0[b * g.h0_stride + dc];
-        }
-    }
+    const int cluster_size = (int)cluster::size(), cluster_rank = (int)cluster::rank();
     // Each CTA's pairs arrive in every CTA's cta_pair by stores that count
     // their bytes on that CTA's barrier; two buffers and barriers by turns.  A
     // buffer is written again two steps on, by a CTA that then has this one's
     // pairs of the step between, sent after it had read the buffer.
     __shared__ __align__(8) uint64_t exchange[2];
     __shared__ int expired;
-    if (csize > 1) {
+    int exchanges = 0;  // so far
+    if (cluster_size > 1) {
         if (tid == 0) {
             mbar_init(smem_u32(&exchange[0]), 1);
             mbar_init(smem_u32(&exchange[1]), 1);
@@ -323,340 +307,397 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
         cluster::sync();  // every CTA's barriers exist before any signals them
     }
 
-    // row r of this thread's slot in staged buffer i
-    auto staged_row = [&](int i, int r) { return staged + i * L::kBufferBytes + (slot * ROWS + r) * L::kPitch; };
-    // How far the 16 bytes that a row's part of this CTA starts in begin before it.
-    auto shift_at = [&](const Walk<const T> &w, int at) {
-        return (uint32_t)(reinterpret_cast<uintptr_t>(w.at) + (uint64_t)((int64_t)at * w.step) * sizeof(T)) & 15u;
-    };
-    // Copies positions base .. base + ROWS - 1 (those below `end`) into buffer i.
-    auto stage = [&](const Walk<const T> &w, const LinrecRows &rows, int base, int end, int i) {
-        const T *p = w.at + base * w.step;
-        if constexpr (!L::SHIFT) {
-#pragma unroll
-            for (int r = 0; r < ROWS; ++r)
-                if (base + r < end) cp_async<16>(staged_row(i, r) + col * 16, p + r * w.step);
-        } else {
-            // every lane a piece, the last one also the ninth; pieces that
-            // reach over the tensor's ends element by element
-            const char *const lo = rows_begin<T>(rows, g), *const hi = rows_end<T>(rows, g);
-            const int64_t bytes = min((int64_t)kChannels, g.D - c0) * (int64_t)sizeof(T);
-#pragma unroll 2
-            for (int r = 0; r < ROWS; ++r) {
-                if (base + r >= end) break;
-                const char *row = reinterpret_cast<const char *>(p + r * w.step) - col * 16;
-                const char *first = reinterpret_cast<const char *>(reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)15);
-                unsigned char *const to = staged_row(i, r);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int k = q ? LANES : col;
-                    const char *from = first + 16 * k;
-                    if ((q && col != LANES - 1) || from >= row + bytes) continue;
-                    if (from >= lo && from + 16 <= hi) {
-                        cp_async<16>(to + 16 * k, from);
-                    } else {
-                        for (int e = 0; e < VEC; ++e)
-                            if (from + e * sizeof(T) >= lo && from + e * sizeof(T) < hi)
-                                reinterpret_cast<T *>(to + 16 * k)[e] = reinterpret_cast<const T *>(from)[e];
-                    }
-                }
-            }
-        }
-    };
-    // This thread's channels of a staged row.
-    auto own = [&](int i, int r, uint32_t shift) {
-        const unsigned char *p = staged_row(i, r) + col * 16;
-        if constexpr (!L::SHIFT) return *reinterpret_cast<const P *>(p);
-        const uint32_t *w = reinterpret_cast<const uint32_t *>(p + (shift & ~3u));
-        uint32_t v[5];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = w[k];
-        if constexpr (sizeof(T) == 2) {
-            if (shift & 2u) {
-                v[4] = w[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = __funnelshift_r(v[k], v[k + 1], 16);
-            }
-        }
-        return *reinterpret_cast<const P *>(v);
-    };
-    // Stores them to their place in memory.
-    auto put = [&](T *p, const P &v) {
-        if constexpr (!L::SHIFT) {
-            store_pack<T, VEC>(p, v);
-        } else if ((reinterpret_cast<uintptr_t>(p) & 3) == 0 && d + VEC <= g.D) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) reinterpret_cast<uint32_t *>(p)[k] = reinterpret_cast<const uint32_t *>(&v)[k];
-        } else {
-#pragma unroll
-            for (int k = 0; k < VEC; ++k)
-                if (d + k < g.D) p[k] = v.v[k];
-        }
-    };
-    const Walk<const T> wg = walk<const T, BWD>(g.gate, seq, d);
-    const Walk<const T> wu = walk<const T, BWD>(BWD ? g.dh : g.x, seq, d);
+    // One sequence's channels `group`, by this CTA as number `crank` of `csize`.
+    auto run = [&](const int64_t b, const int64_t group, const int csize, const int crank) {
+        const int64_t c0 = group * kChannels;
+        const int64_t d = c0 + col * VEC;
+        const bool live = d < g.D;
+        const Sequence seq = sequence(g, b);
+        const int len = live ? seq.len : 0;  // tokens that this thread walks
+        // and copies: a piece may hold channels of the lane before only
+        const int copy_len = L::SHIFT ? seq.len : len;
 
-    // T is at most 2^31 - 2^16: positions past the end by two steps fit an int
-    const int step = csize * kStretch;
-    const int steps = (seq.len + step - 1) / step;
-    int base = crank * kStretch + slot * ROWS;  // this thread's first position
-    // the next step's gate and x (dh) into buffer pair `i`
-    auto stage_next = [&](int at, int i) {
-        stage(wg, g.gate, at, copy_len, 2 * i);
-        stage(wu, BWD ? g.dh : g.x, at, copy_len, 2 * i + 1);
-    };
-    // for the backward pass's second walk: the row before each token (the last
-    // position is row 0, whose state before is h0), and x
-    auto stage_side = [&](int at) {
-        if constexpr (BWD && L::SIDE) {
-            const Walk<const T> wh = walk<const T, BWD>(g.h, seq, d);
-            stage({wh.at + wh.step, wh.step}, g.h, at, copy_len - 1, 2 * L::STAGES);
-            if constexpr (kSigmoid) stage(walk<const T, BWD>(g.x, seq, d), g.x, at, copy_len, 2 * L::STAGES + 1);
+        // each of them carries the state of its channel from step to step
+        const int64_t dc = c0 + L::channel_at(place);
+        float carry = 0.f;
+        if (dc < g.D) {
+            if constexpr (BWD) {
+                if (g.dh_last) carry = g.dh_last[b * g.D + dc];
+            } else {
+                if (g.h0) carry = g.h0[b * g.h0_stride + dc];
+            }
         }
-    };
-    stage_next(base, 0);
-    stage_side(base);
-    cp_async_commit();
-    int parity = 0, i = 0;
-    for (; i < steps; ++i, base += step, parity ^= 1) {
-        const int bg = L::STAGES == 2 ? 2 * parity : 0, bu = bg + 1;  // this step's buffers
-        if constexpr (L::SHIFT) __syncwarp();  // the lanes of a row have read each other's pieces
-        P rh[BWD && !L::SIDE ? ROWS : 1], rx[BWD && !L::SIDE && kSigmoid ? ROWS : 1];
-        if constexpr (BWD && !L::SIDE) {
-            const Walk<const T> wh = walk<const T, BWD>(g.h, seq, d);
-            const T *ph = wh.at + (base + 1) * wh.step;
-#pragma unroll
-            for (int r = 0; r < ROWS; ++r)
-                if (base + r + 1 < len) rh[r] = load_once<T, VEC>(ph + r * wh.step);
-            if constexpr (kSigmoid) {
-                const Walk<const T> wx = walk<const T, BWD>(g.x, seq, d);
-                const T *px = wx.at + base * wx.step;
+
+        // row r of this thread's slot in staged buffer i
+        auto staged_row = [&](int i, int r) { return staged + i * L::kBufferBytes + (slot * ROWS + r) * L::kPitch; };
+        // How far the 16 bytes that a row's part of this CTA starts in begin before it.
+        auto shift_at = [&](const Walk<const T> &w, int at) {
+            return (uint32_t)(reinterpret_cast<uintptr_t>(w.at) + (uint64_t)((int64_t)at * w.step) * sizeof(T)) & 15u;
+        };
+        // Copies positions base .. base + ROWS - 1 (those below `end`) into buffer i.
+        auto stage = [&](const Walk<const T> &w, const LinrecRows &rows, int base, int end, int i) {
+            const T *p = w.at + base * w.step;
+            if constexpr (!L::SHIFT) {
 #pragma unroll
                 for (int r = 0; r < ROWS; ++r)
-                    if (base + r < len) rx[r] = load_once<T, VEC>(px + r * wx.step);
-            }
-        }
-        if constexpr (L::STAGES == 2) {
-            stage_next(base + step, parity ^ 1);
-            cp_async_commit();
-            cp_async_wait<1>();
-        } else {
-            cp_async_wait<0>();
-        }
-        if constexpr (L::SHIFT) __syncwarp();
-        // the shifts of this thread's rows; the same for the side inputs below
-        const uint32_t shift_g = L::SHIFT ? shift_at(wg, base) - col * 16 : 0, shift_u = L::SHIFT ? shift_at(wu, base) - col * 16 : 0;
-        const uint32_t next_g = (uint32_t)(wg.step * (int64_t)sizeof(T)), next_u = (uint32_t)(wu.step * (int64_t)sizeof(T));
-
-        // first walk: (A, H) of the slot
-        V a[kKeep ? ROWS : 1][kN], u[kKeep ? ROWS : 1][kN], A[kN], H[kN];
+                    if (base + r < end) cp_async<16>(staged_row(i, r) + col * 16, p + r * w.step);
+            } else {
+                // every lane a piece, the last one also the ninth; pieces that
+                // reach over the tensor's ends element by element
+                const char *const lo = rows_begin<T>(rows, g), *const hi = rows_end<T>(rows, g);
+                const int64_t bytes = min((int64_t)kChannels, g.D - c0) * (int64_t)sizeof(T);
+#pragma unroll 2
+                for (int r = 0; r < ROWS; ++r) {
+                    if (base + r >= end) break;
+                    const char *row = reinterpret_cast<const char *>(p + r * w.step) - col * 16;
+                    const char *first = reinterpret_cast<const char *>(reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)15);
+                    unsigned char *const to = staged_row(i, r);
 #pragma unroll
-        for (int k = 0; k < kN; ++k) {
-            A[k] = splat<V>(1.f);
-            H[k] = splat<V>(0.f);
-        }
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            if (base + r < len) {
-                const P q = own(bg, r, (shift_g + r * next_g) & 15u), e = own(bu, r, (shift_u + r * next_u) & 15u);
-#pragma unroll
-                for (int k = 0; k < kN; ++k) {
-                    V at, rest, ut = value(e, k);
-                    open_gate<T, FORM>(value(q, k), at, rest);
-                    if constexpr (kSigmoid && !BWD) ut = mul_(ut, rest);
-                    H[k] = BWD ? mul_(at, add_(H[k], ut)) : mad_(at, H[k], ut);
-                    A[k] = mul_(A[k], at);
-                    if constexpr (kKeep) {
-                        a[r][k] = at;
-                        u[r][k] = ut;
-                    }
-                }
-            }
-        }
-
-        // (A, H) of the slots -> of the parts -> of the CTA -> of the CTAs
-        // before; then back down to the state each slot starts from
-        constexpr int kQuad = VEC < 4 ? VEC : 4;
-#pragma unroll
-        for (int v = 0; v < VEC; v += kQuad) {
-            const int at = v * LANES + col * kQuad;
-            Pack<float, kQuad> qa, qh;
-#pragma unroll
-            for (int k = 0; k < (kQuad + 1) / 2; ++k) {
-                set_value(qa, k, A[(v + 1) / 2 + k]);
-                set_value(qh, k, H[(v + 1) / 2 + k]);
-            }
-            store_pack<float, kQuad>(&slot_A[slot][at], qa);
-            store_pack<float, kQuad>(&slot_H[slot][at], qh);
-        }
-        __syncthreads();
-        float sa[kPartSlots], sh[kPartSlots];
-        {
-            float pa = 1.f, ph = 0.f;
-#pragma unroll
-            for (int k = 0; k < kPartSlots; ++k) {
-                sa[k] = slot_A[part * kPartSlots + k][place];
-                sh[k] = slot_H[part * kPartSlots + k][place];
-                ph = apply(sa[k], sh[k], ph);
-                pa *= sa[k];
-            }
-            part_pair[part][place] = make_float2(pa, ph);
-        }
-        __syncthreads();
-        float2 parts[kParts];
-#pragma unroll
-        for (int k = 0; k < kParts; ++k) parts[k] = part_pair[k][place];
-        float state = carry;
-        if (csize > 1) {
-            float ca = 1.f, ch = 0.f;
-#pragma unroll
-            for (int k = 0; k < kParts; ++k) {
-                ch = apply(parts[k].x, parts[k].y, ch);
-                ca *= parts[k].x;
-            }
-            const uint32_t at = smem_u32(&cta_pair[parity][crank][place]), bar = smem_u32(&exchange[parity]);
-            if (tid == 0) mbar_expect_tx(bar, (uint32_t)(csize * kChannels * sizeof(float2)));
-            for (int k = part; k < csize; k += kParts)
-                cluster::send_f32x2(cluster::map(at, k), ca, ch, cluster::map(bar, k));
-            if (!cluster::wait(bar, (i >> 1) & 1, g.wait_limit)) {
-                record_timeout(g.status);
-                *(volatile int *)&expired = 1;
-            }
-            float2 ctas[kMaxCluster];
-#pragma unroll
-            for (int k = 0; k < kMaxCluster; ++k)
-                if (k < csize) ctas[k] = cta_pair[parity][k][place];
-#pragma unroll
-            for (int k = 0; k < kMaxCluster; ++k) {
-                if (k == crank) state = carry;
-                if (k < csize) carry = apply(ctas[k].x, ctas[k].y, carry);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kParts; ++k) {
-            if (k < part) state = apply(parts[k].x, parts[k].y, state);
-            if (csize == 1) carry = apply(parts[k].x, parts[k].y, carry);
-        }
-#pragma unroll
-        for (int k = 0; k < kPartSlots; ++k) {
-            slot_H[part * kPartSlots + k][place] = state;
-            state = apply(sa[k], sh[k], state);
-        }
-        __syncthreads();
-        if (csize > 1 && *(volatile int *)&expired) break;  // seen by all threads alike
-
-        // second walk, from the slot's starting state
-        V h[kN];
-#pragma unroll
-        for (int v = 0; v < VEC; v += kQuad) {
-            const Pack<float, kQuad> q = load_pack<float, kQuad>(&slot_H[slot][v * LANES + col * kQuad]);
-#pragma unroll
-            for (int k = 0; k < (kQuad + 1) / 2; ++k) h[(v + 1) / 2 + k] = value(q, k);
-        }
-        if constexpr (!BWD) {
-            const Walk<T> wo = walk<T, BWD>(g.h, seq, d);
-            T *out = wo.at + base * wo.step;
-#pragma unroll
-            for (int r = 0; r < ROWS; ++r) {
-                if (base + r < len) {
-                    P o, q, e;
-                    if constexpr (!kKeep) {
-                        q = own(bg, r, (shift_g + r * next_g) & 15u);
-                        e = own(bu, r, (shift_u + r * next_u) & 15u);
-                    }
-#pragma unroll
-                    for (int k = 0; k < kN; ++k) {
-                        V at, ut, rest;
-                        if constexpr (kKeep) {
-                            at = a[r][k];
-                            ut = u[r][k];
+                    for (int q = 0; q < 2; ++q) {
+                        const int k = q ? LANES : col;
+                        const char *from = first + 16 * k;
+                        if ((q && col != LANES - 1) || from >= row + bytes) continue;
+                        if (from >= lo && from + 16 <= hi) {
+                            cp_async<16>(to + 16 * k, from);
                         } else {
-                            open_gate<T, FORM>(value(q, k), at, rest);
-                            ut = value(e, k);
-                            if constexpr (kSigmoid) ut = mul_(ut, rest);
+                            for (int e = 0; e < VEC; ++e)
+                                if (from + e * sizeof(T) >= lo && from + e * sizeof(T) < hi)
+                                    reinterpret_cast<T *>(to + 16 * k)[e] = reinterpret_cast<const T *>(from)[e];
                         }
-                        h[k] = mad_(at, h[k], ut);
-                        set_value(o, k, h[k]);
                     }
-                    put(out + r * wo.step, o);
                 }
             }
-        } else {
-            const Walk<T> wo = walk<T, BWD>(g.dgate, seq, d), wx = walk<T, BWD>(g.dx, seq, d);
-            T *og = wo.at + base * wo.step, *ox = wx.at + base * wx.step;
-            uint32_t shift_h = 0, shift_x = 0, next_h = 0, next_x = 0;
-            if constexpr (L::SHIFT) {
-                const Walk<const T> wh = walk<const T, BWD>(g.h, seq, d);
-                shift_h = shift_at(wh, base + 1) - col * 16;
-                next_h = (uint32_t)(wh.step * (int64_t)sizeof(T));
-                if constexpr (kSigmoid) {
-                    const Walk<const T> wi = walk<const T, BWD>(g.x, seq, d);
-                    shift_x = shift_at(wi, base) - col * 16;
-                    next_x = (uint32_t)(wi.step * (int64_t)sizeof(T));
+        };
+        // This thread's channels of a staged row.
+        auto own = [&](int i, int r, uint32_t shift) {
+            const unsigned char *p = staged_row(i, r) + col * 16;
+            if constexpr (!L::SHIFT) return *reinterpret_cast<const P *>(p);
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(p + (shift & ~3u));
+            uint32_t v[5];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = w[k];
+            if constexpr (sizeof(T) == 2) {
+                if (shift & 2u) {
+                    v[4] = w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = __funnelshift_r(v[k], v[k + 1], 16);
                 }
+            }
+            return *reinterpret_cast<const P *>(v);
+        };
+        // Stores them to their place in memory.
+        auto put = [&](T *p, const P &v) {
+            if constexpr (!L::SHIFT) {
+                store_pack<T, VEC>(p, v);
+            } else if ((reinterpret_cast<uintptr_t>(p) & 3) == 0 && d + VEC <= g.D) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) reinterpret_cast<uint32_t *>(p)[k] = reinterpret_cast<const uint32_t *>(&v)[k];
+            } else {
+#pragma unroll
+                for (int k = 0; k < VEC; ++k)
+                    if (d + k < g.D) p[k] = v.v[k];
+            }
+        };
+        const Walk<const T> wg = walk<const T, BWD>(g.gate, seq, d);
+        const Walk<const T> wu = walk<const T, BWD>(BWD ? g.dh : g.x, seq, d);
+
+        // T is at most 2^31 - 2^16: positions past the end by two steps fit an int
+        const int step = csize * kStretch;
+        const int steps = (seq.len + step - 1) / step;
+        int base = crank * kStretch + slot * ROWS;  // this thread's first position
+        // the next step's gate and x (dh) into buffer pair `i`
+        auto stage_next = [&](int at, int i) {
+            stage(wg, g.gate, at, copy_len, 2 * i);
+            stage(wu, BWD ? g.dh : g.x, at, copy_len, 2 * i + 1);
+        };
+        // for the backward pass's second walk: the row before each token (the last
+        // position is row 0, whose state before is h0), and x
+        auto stage_side = [&](int at) {
+            if constexpr (BWD && L::SIDE) {
+                const Walk<const T> wh = walk<const T, BWD>(g.h, seq, d);
+                stage({wh.at + wh.step, wh.step}, g.h, at, copy_len - 1, 2 * L::STAGES);
+                if constexpr (kSigmoid) stage(walk<const T, BWD>(g.x, seq, d), g.x, at, copy_len, 2 * L::STAGES + 1);
+            }
+        };
+        stage_next(base, 0);
+        stage_side(base);
+        cp_async_commit();
+        int parity = 0, i = 0;
+        for (; i < steps; ++i, base += step, parity ^= 1) {
+            const int bg = L::STAGES == 2 ? 2 * parity : 0, bu = bg + 1;  // this step's buffers
+            if constexpr (L::SHIFT) __syncwarp();  // the lanes of a row have read each other's pieces
+            P rh[BWD && !L::SIDE ? ROWS : 1], rx[BWD && !L::SIDE && kSigmoid ? ROWS : 1];
+            if constexpr (BWD && !L::SIDE) {
+                const Walk<const T> wh = walk<const T, BWD>(g.h, seq, d);
+                const T *ph = wh.at + (base + 1) * wh.step;
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r)
+                    if (base + r + 1 < len) rh[r] = load_once<T, VEC>(ph + r * wh.step);
+                if constexpr (kSigmoid) {
+                    const Walk<const T> wx = walk<const T, BWD>(g.x, seq, d);
+                    const T *px = wx.at + base * wx.step;
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r)
+                        if (base + r < len) rx[r] = load_once<T, VEC>(px + r * wx.step);
+                }
+            }
+            if constexpr (L::STAGES == 2) {
+                stage_next(base + step, parity ^ 1);
+                cp_async_commit();
+                cp_async_wait<1>();
+            } else {
+                cp_async_wait<0>();
+            }
+            if constexpr (L::SHIFT) __syncwarp();
+            // the shifts of this thread's rows; the same for the side inputs below
+            const uint32_t shift_g = L::SHIFT ? shift_at(wg, base) - col * 16 : 0, shift_u = L::SHIFT ? shift_at(wu, base) - col * 16 : 0;
+            const uint32_t next_g = (uint32_t)(wg.step * (int64_t)sizeof(T)), next_u = (uint32_t)(wu.step * (int64_t)sizeof(T));
+
+            // first walk: (A, H) of the slot
+            V a[kKeep ? ROWS : 1][kN], u[kKeep ? ROWS : 1][kN], A[kN], H[kN];
+#pragma unroll
+            for (int k = 0; k < kN; ++k) {
+                A[k] = splat<V>(1.f);
+                H[k] = splat<V>(0.f);
             }
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
                 if (base + r < len) {
                     const P q = own(bg, r, (shift_g + r * next_g) & 15u), e = own(bu, r, (shift_u + r * next_u) & 15u);
-                    P o0, o1, before, in;
-                    if constexpr (L::SIDE) {
-                        before = own(2 * L::STAGES, r, (shift_h + r * next_h) & 15u);
-                        if constexpr (kSigmoid) in = own(2 * L::STAGES + 1, r, (shift_x + r * next_x) & 15u);
-                    } else {
-                        before = rh[r];
-                        if constexpr (kSigmoid) in = rx[r];
-                    }
-                    const bool start = base + r + 1 == len;  // row 0: the state before it is h0
-                    Pack<float, VEC> first = {};
-                    if (start && g.h0) {
-#pragma unroll
-                        for (int v = 0; v < VEC; ++v)
-                            if (!L::SHIFT || d + v < g.D) first.v[v] = g.h0[b * g.h0_stride + d + v];
-                    }
 #pragma unroll
                     for (int k = 0; k < kN; ++k) {
-                        V at, rest;
+                        V at, rest, ut = value(e, k);
                         open_gate<T, FORM>(value(q, k), at, rest);
-                        const V prev = start ? value(first, k) : value(before, k);
-                        const V full = add_(value(e, k), h[k]);
-                        h[k] = mul_(at, full);
-                        if constexpr (FORM == TRSM_GATE_DECAY) {
-                            set_value(o0, k, mul_(full, prev));
-                            set_value(o1, k, full);
-                        } else if constexpr (FORM == TRSM_GATE_LOG) {
-                            set_value(o0, k, mul_(h[k], prev));
-                            set_value(o1, k, full);
-                        } else {
-                            const V gap = mad_(value(in, k), splat<V>(-1.f), prev);
-                            set_value(o0, k, mul_(gap, mul_(h[k], rest)));
-                            set_value(o1, k, mul_(full, rest));
+                        if constexpr (kSigmoid && !BWD) ut = mul_(ut, rest);
+                        H[k] = BWD ? mul_(at, add_(H[k], ut)) : mad_(at, H[k], ut);
+                        A[k] = mul_(A[k], at);
+                        if constexpr (kKeep) {
+                            a[r][k] = at;
+                            u[r][k] = ut;
                         }
                     }
-                    put(og + r * wo.step, o0);
-                    put(ox + r * wx.step, o1);
+                }
+            }
+
+            // (A, H) of the slots -> of the parts -> of the CTA -> of the CTAs
+            // before; then back down to the state each slot starts from
+            constexpr int kQuad = VEC < 4 ? VEC : 4;
+#pragma unroll
+            for (int v = 0; v < VEC; v += kQuad) {
+                const int at = v * LANES + col * kQuad;
+                Pack<float, kQuad> qa, qh;
+#pragma unroll
+                for (int k = 0; k < (kQuad + 1) / 2; ++k) {
+                    set_value(qa, k, A[(v + 1) / 2 + k]);
+                    set_value(qh, k, H[(v + 1) / 2 + k]);
+                }
+                store_pack<float, kQuad>(&slot_A[slot][at], qa);
+                store_pack<float, kQuad>(&slot_H[slot][at], qh);
+            }
+            __syncthreads();
+            float sa[kPartSlots], sh[kPartSlots];
+            {
+                float pa = 1.f, ph = 0.f;
+#pragma unroll
+                for (int k = 0; k < kPartSlots; ++k) {
+                    sa[k] = slot_A[part * kPartSlots + k][place];
+                    sh[k] = slot_H[part * kPartSlots + k][place];
+                    ph = apply(sa[k], sh[k], ph);
+                    pa *= sa[k];
+                }
+                part_pair[part][place] = make_float2(pa, ph);
+            }
+            __syncthreads();
+            float2 parts[kParts];
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) parts[k] = part_pair[k][place];
+            float state = carry;
+            if (csize > 1) {
+                float ca = 1.f, ch = 0.f;
+#pragma unroll
+                for (int k = 0; k < kParts; ++k) {
+                    ch = apply(parts[k].x, parts[k].y, ch);
+                    ca *= parts[k].x;
+                }
+                const uint32_t at = smem_u32(&cta_pair[exchanges & 1][crank][place]);
+                const uint32_t bar = smem_u32(&exchange[exchanges & 1]);
+                if (tid == 0) mbar_expect_tx(bar, (uint32_t)(csize * kChannels * sizeof(float2)));
+                for (int k = part; k < csize; k += kParts)
+                    cluster::send_f32x2(cluster::map(at, k), ca, ch, cluster::map(bar, k));
+                if (!cluster::wait(bar, (exchanges >> 1) & 1, g.wait_limit)) {
+                    record_timeout(g.status);
+                    *(volatile int *)&expired = 1;
+                }
+                float2 ctas[kMaxCluster];
+#pragma unroll
+                for (int k = 0; k < kMaxCluster; ++k)
+                    if (k < csize) ctas[k] = cta_pair[exchanges & 1][k][place];
+#pragma unroll
+                for (int k = 0; k < kMaxCluster; ++k) {
+                    if (k == crank) state = carry;
+                    if (k < csize) carry = apply(ctas[k].x, ctas[k].y, carry);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) {
+                if (k < part) state = apply(parts[k].x, parts[k].y, state);
+                if (csize == 1) carry = apply(parts[k].x, parts[k].y, carry);
+            }
+#pragma unroll
+            for (int k = 0; k < kPartSlots; ++k) {
+                slot_H[part * kPartSlots + k][place] = state;
+                state = apply(sa[k], sh[k], state);
+            }
+            __syncthreads();
+            if (csize > 1) {
+                ++exchanges;
+                if (*(volatile int *)&expired) return;  // seen by all threads alike
+            }
+
+            // second walk, from the slot's starting state
+            V h[kN];
+#pragma unroll
+            for (int v = 0; v < VEC; v += kQuad) {
+                const Pack<float, kQuad> q = load_pack<float, kQuad>(&slot_H[slot][v * LANES + col * kQuad]);
+#pragma unroll
+                for (int k = 0; k < (kQuad + 1) / 2; ++k) h[(v + 1) / 2 + k] = value(q, k);
+            }
+            if constexpr (!BWD) {
+                const Walk<T> wo = walk<T, BWD>(g.h, seq, d);
+                T *out = wo.at + base * wo.step;
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) {
+                    if (base + r < len) {
+                        P o, q, e;
+                        if constexpr (!kKeep) {
+                            q = own(bg, r, (shift_g + r * next_g) & 15u);
+                            e = own(bu, r, (shift_u + r * next_u) & 15u);
+                        }
+#pragma unroll
+                        for (int k = 0; k < kN; ++k) {
+                            V at, ut, rest;
+                            if constexpr (kKeep) {
+                                at = a[r][k];
+                                ut = u[r][k];
+                            } else {
+                                open_gate<T, FORM>(value(q, k), at, rest);
+                                ut = value(e, k);
+                                if constexpr (kSigmoid) ut = mul_(ut, rest);
+                            }
+                            h[k] = mad_(at, h[k], ut);
+                            set_value(o, k, h[k]);
+                        }
+                        put(out + r * wo.step, o);
+                    }
+                }
+            } else {
+                const Walk<T> wo = walk<T, BWD>(g.dgate, seq, d), wx = walk<T, BWD>(g.dx, seq, d);
+                T *og = wo.at + base * wo.step, *ox = wx.at + base * wx.step;
+                uint32_t shift_h = 0, shift_x = 0, next_h = 0, next_x = 0;
+                if constexpr (L::SHIFT) {
+                    const Walk<const T> wh = walk<const T, BWD>(g.h, seq, d);
+                    shift_h = shift_at(wh, base + 1) - col * 16;
+                    next_h = (uint32_t)(wh.step * (int64_t)sizeof(T));
+                    if constexpr (kSigmoid) {
+                        const Walk<const T> wi = walk<const T, BWD>(g.x, seq, d);
+                        shift_x = shift_at(wi, base) - col * 16;
+                        next_x = (uint32_t)(wi.step * (int64_t)sizeof(T));
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) {
+                    if (base + r < len) {
+                        const P q = own(bg, r, (shift_g + r * next_g) & 15u), e = own(bu, r, (shift_u + r * next_u) & 15u);
+                        P o0, o1, before, in;
+                        if constexpr (L::SIDE) {
+                            before = own(2 * L::STAGES, r, (shift_h + r * next_h) & 15u);
+                            if constexpr (kSigmoid) in = own(2 * L::STAGES + 1, r, (shift_x + r * next_x) & 15u);
+                        } else {
+                            before = rh[r];
+                            if constexpr (kSigmoid) in = rx[r];
+                        }
+                        const bool start = base + r + 1 == len;  // row 0: the state before it is h0
+                        Pack<float, VEC> first = {};
+                        if (start && g.h0) {
+#pragma unroll
+                            for (int v = 0; v < VEC; ++v)
+                                if (!L::SHIFT || d + v < g.D) first.v[v] = g.h0[b * g.h0_stride + d + v];
+                        }
+#pragma unroll
+                        for (int k = 0; k < kN; ++k) {
+                            V at, rest;
+                            open_gate<T, FORM>(value(q, k), at, rest);
+                            const V prev = start ? value(first, k) : value(before, k);
+                            const V full = add_(value(e, k), h[k]);
+                            h[k] = mul_(at, full);
+                            if constexpr (FORM == TRSM_GATE_DECAY) {
+                                set_value(o0, k, mul_(full, prev));
+                                set_value(o1, k, full);
+                            } else if constexpr (FORM == TRSM_GATE_LOG) {
+                                set_value(o0, k, mul_(h[k], prev));
+                                set_value(o1, k, full);
+                            } else {
+                                const V gap = mad_(value(in, k), splat<V>(-1.f), prev);
+                                set_value(o0, k, mul_(gap, mul_(h[k], rest)));
+                                set_value(o1, k, mul_(full, rest));
+                            }
+                        }
+                        put(og + r * wo.step, o0);
+                        put(ox + r * wx.step, o1);
+                    }
+                }
+            }
+            if constexpr (L::SHIFT) __syncwarp();
+            if constexpr (L::STAGES == 1) {  // this thread (SHIFT: row) has been read
+                stage_next(base + step, 0);
+                if constexpr (L::SIDE) stage_side(base + step);
+                cp_async_commit();
+            } else if constexpr (L::SIDE) {
+                stage_side(base + step);
+                cp_async_commit();
+            }
+        }
+        if (g.last && crank == 0 && part == 0 && dc < g.D) g.last[b * g.D + dc] = carry;
+        if constexpr (L::SHIFT) __syncwarp();  // before the next sequence's copies
+    };
+
+    // A batch has one sequence's channels for each cluster.  Packed sequences
+    // are of any lengths, which the host does not know: the long ones are dealt
+    // out to the clusters, then the short ones to the CTAs.
+    const int64_t cluster_id = blockIdx.x / cluster_size;
+    bool given_up = false;
+    if constexpr (!PACKED) {
+        run(cluster_id / groups, cluster_id % groups, cluster_size, cluster_rank);
+        given_up = cluster_size > 1 && *(volatile int *)&expired;
+    } else {
+        for (int pass = 0; pass < 2 && !given_up; ++pass) {
+            const int csize = pass ? 1 : cluster_size, crank = pass ? 0 : cluster_rank;
+            const int64_t stride = pass ? gridDim.x : gridDim.x / cluster_size;
+            int64_t next = pass ? blockIdx.x : cluster_id;  // of those dealt out
+            for (int64_t b0 = 0; b0 < g.batch && !given_up; b0 += 32) {
+                const int64_t mine = b0 + (tid & 31);
+                const bool is_long = mine < g.batch && sequence(g, mine).len > kLong * kStretch;
+                uint32_t todo = __ballot_sync(~0u, mine < g.batch && is_long == (pass == 0));
+                for (; todo && !given_up; todo &= todo - 1) {
+                    const int64_t b = b0 + __ffs(todo) - 1;
+                    for (; next < groups && !given_up; next += stride) {
+                        run(b, next, csize, crank);
+                        given_up = cluster_size > 1 && *(volatile int *)&expired;
+                    }
+                    next -= groups;
                 }
             }
         }
-        if constexpr (L::SHIFT) __syncwarp();
-        if constexpr (L::STAGES == 1) {  // this thread (SHIFT: row) has been read
-            stage_next(base + step, 0);
-            if constexpr (L::SIDE) stage_side(base + step);
-            cp_async_commit();
-        } else if constexpr (L::SIDE) {
-            stage_side(base + step);
-            cp_async_commit();
-        }
     }
     cp_async_wait_all();
-    if (csize > 1) {
+    if (cluster_size > 1) {
         cluster::sync();  // no CTA leaves while another may still send to it
-        if (*(volatile int *)&expired) {  // ... nor before what was sent has landed
-            if (tid == 0) cluster::wait(smem_u32(&exchange[parity]), (i >> 1) & 1, kWaitLimit);
+        if (given_up) {  // ... nor before what was sent has landed
+            --exchanges;
+            if (tid == 0) cluster::wait(smem_u32(&exchange[exchanges & 1]), (exchanges >> 1) & 1, kWaitLimit);
             __syncthreads();
         }
     }
-    if (g.last && crank == 0 && part == 0 && dc < g.D) g.last[b * g.D + dc] = carry;
 }
 
 // One token per row: y = next[s] = a state[s] + u.
@@ -716,7 +757,7 @@ inline bool rows_vec(const LinrecArgs &a, const LinrecRows &r, int64_t elem) {
     return bits % 16 == 0;
 }
 
-template <typename T, int FORM, bool BWD, typename L>
+template <typename T, int FORM, bool BWD, bool PACKED, typename L>
 int launch_scan(LinrecArgs a, cudaStream_t st) {
     constexpr size_t kSmem = L::template smem<T, FORM, BWD>();
     int sms = 0;
@@ -726,17 +767,24 @@ int launch_scan(LinrecArgs a, cudaStream_t st) {
     if (rc) return rc;
     const int64_t groups = (a.D + L::kChannels - 1) / L::kChannels;
     const int64_t units = a.batch * groups;
-    // CTAs along a sequence: until the GPU is full, but no more than it has stretches
-    const int64_t len = a.offsets ? (a.T + a.batch - 1) / a.batch : a.T;
     int cs = 1;
-    while (cs < kMaxCluster && units * cs < 4 * sms && cs * L::kStretch < len) cs *= 2;
-    if (units * cs > 0x7fffffff) return -3;
-    auto *kernel = scan_kernel<T, FORM, BWD, L>;
+    int64_t clusters = units;
+    if (!PACKED) {
+        // CTAs along a sequence: until the GPU is full, but no more than it has stretches
+        while (cs < kMaxCluster && units * cs < 4 * sms && cs * L::kStretch < a.T) cs *= 2;
+    } else {
+        // as many as the longest could use; the clusters that run at once share the work
+        while (cs < kMaxCluster && cs * L::kStretch < a.T) cs *= 2;
+        const int64_t most = 2 * sms / cs;
+        if (clusters > most) clusters = most;
+    }
+    if (clusters * cs > 0x7fffffff) return -3;
+    auto *kernel = scan_kernel<T, FORM, BWD, PACKED, L>;
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return cuda_status(e);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * cs));
+    cfg.gridDim = dim3((unsigned)(clusters * cs));
     cfg.blockDim = dim3(L::kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
@@ -749,15 +797,31 @@ int launch_scan(LinrecArgs a, cudaStream_t st) {
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, a, (int)groups));
 }
 
-template <typename T, int FORM, bool BWD>
-int run(const LinrecArgs &a, cudaStream_t st) {
-    constexpr int kVec = 16 / sizeof(T);
+template <typename T, int FORM, bool BWD, bool PACKED>
+int run_layout(const LinrecArgs &a, cudaStream_t st) {
+    constexpr int kVec = 16 / sizeof(T), kRows = 32 / kVec;
     bool vec = a.D % kVec == 0 && rows_vec(a, a.gate, sizeof(T)) && rows_vec(a, a.h, sizeof(T));
     if (!BWD || FORM == TRSM_GATE_SIGMOID) vec = vec && rows_vec(a, a.x, sizeof(T));
     if (BWD) vec = vec && rows_vec(a, a.dh, sizeof(T)) && rows_vec(a, a.dgate, sizeof(T)) && rows_vec(a, a.dx, sizeof(T));
-    constexpr int kRows = 32 / kVec;
-    if (vec) return launch_scan<T, FORM, BWD, Plan<kVec, 8, 256, kRows, 2, false, false, 2>>(a, st);
-    return launch_scan<T, FORM, BWD, Plan<kVec, 8, 256, kRows, BWD ? 1 : 2, true, true, 2>>(a, st);
+    // Rows off the 16-byte boundaries: 256 threads (1 x 65536 x 2047 bf16 505
+    // us, 4 x 2048 x 2047 76 us; 128 threads 593 and 64).
+    if (!vec) return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 8, 256, kRows, BWD ? 1 : 2, true, true, 2>>(a, st);
+    // Otherwise 128 threads, and as many channels a CTA as leave the GPU full
+    // with clusters of eight: 4 x 2048 x 2048 29 us with 8 lanes, 46 with 4; 1 x
+    // 65536 x 2048 198 us with 4 lanes, 232 with 8; 1 x 65536 x 512 85 us with 2
+    // lanes, 129 with 4.  Packed sequences are few long ones as far as the host
+    // knows.
+    auto units = [&](int lanes) { return a.batch * ((a.D + lanes * kVec - 1) / (lanes * kVec)); };
+    if constexpr (!PACKED) {
+        if (units(8) >= 64) return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 8, 128, kRows, 2, false, false, 4>>(a, st);
+        if (units(4) < 64) return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 2, 128, kRows, 2, false, false, 4>>(a, st);
+    }
+    return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 4, 128, kRows, 2, false, false, 4>>(a, st);
+}
+
+template <typename T, int FORM, bool BWD>
+int run(const LinrecArgs &a, cudaStream_t st) {
+    return a.offsets ? run_layout<T, FORM, BWD, true>(a, st) : run_layout<T, FORM, BWD, false>(a, st);
 }
 
 template <typename T>
