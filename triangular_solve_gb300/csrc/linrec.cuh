@@ -780,9 +780,15 @@ int launch_scan(LinrecArgs a, cudaStream_t st) {
     }
     if (clusters * cs > 0x7fffffff) return -3;
     auto *kernel = scan_kernel<T, FORM, BWD, PACKED, L>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    // once per device; doing it twice does no harm
+    static bool allowed[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
+    if (e == cudaSuccess && !allowed[dev])
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return cuda_status(e);
+    allowed[dev] = true;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * cs));
     cfg.blockDim = dim3(L::kThreads);

@@ -84,6 +84,8 @@ def _coefficients(steps, coef):
     keeps the library's."""
     if coef is None:
         return None
+    if len(coef) == 3 and steps and not hasattr(coef[0], "__len__"):
+        return (ctypes.c_double * (3 * steps))(*(tuple(coef) * steps))
     flat = [float(v) for t in coef for v in (t if hasattr(t, "__len__") else (t,))]
     if len(flat) == 3:
         flat = flat * steps
@@ -109,26 +111,30 @@ def trsm_orthogonalize_workspace_bytes(in_dtype, m, n, batch, steps=5) -> int:
 
 
 # ------------------------------------------------------------------ torch tensors
-_torch = None
+_torch = _f32 = _empty = _current_device = _current_stream = None
 _elem = {}
 
 
 def _load_torch():
-    global _torch
+    """torch, with what the calls below use of it at hand: a call's own work on
+    the host is a good part of a small one's time."""
+    global _torch, _f32, _empty, _current_device, _current_stream
     if _torch is None:
         import torch
         _elem.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+        _f32, _empty = torch.float32, torch.empty
+        _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        _library()
         _torch = torch
     return _torch
 
 
 def _launch(fn, dev, *args):
     """Calls entry point `fn` with device `dev` current, on its current stream."""
-    cuda = _torch._C
-    if dev == cuda._cuda_getDevice():
-        return fn(*args, cuda._cuda_getCurrentRawStream(dev))
+    if dev == _current_device():
+        return fn(*args, _current_stream(dev))
     with _torch.cuda.device(dev):
-        return fn(*args, cuda._cuda_getCurrentRawStream(dev))
+        return fn(*args, _current_stream(dev))
 
 
 def _refuse(name, t, shape, dtype, dev):
@@ -147,7 +153,7 @@ def _refuse(name, t, shape, dtype, dev):
 def _rows(name, t, shape, dtype, dev):
     """Pointer and strides (batch, token) of a tensor like the gate."""
     st = t.stride()
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or st[-1] != 1:
+    if st[-1] != 1 or t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
         _refuse(name, t, shape, dtype, dev)
     return (t.data_ptr(), st[0], st[1]) if len(st) == 3 else (t.data_ptr(), 0, st[0])
 
@@ -157,8 +163,8 @@ def _state(name, t, shape, dev):
     if t is None:
         return None, 0
     st = t.stride()
-    if t.dtype is not _torch.float32 or t.shape != shape or t.get_device() != dev or st[-1] != 1:
-        _refuse(name, t, shape, _torch.float32, dev)
+    if t.dtype is not _f32 or t.get_device() != dev or t.shape != shape or st[-1] != 1:
+        _refuse(name, t, shape, _f32, dev)
     return t.data_ptr(), st[0]
 
 
@@ -186,14 +192,15 @@ def _gate(gate, offsets):
 
 
 def _forward(gate, x, h0, form, offsets):
-    torch = _load_torch()
+    if _torch is None:
+        _load_torch()
     code, batch, T, D, dev, po = _gate(gate, offsets)
-    kind = _code(FORMS, form, "form")
-    shape, dtype = gate.shape, gate.dtype
+    kind = FORMS[form] if form in FORMS else _code(FORMS, form, "form")
+    shape, dtype, device = gate.shape, gate.dtype, gate.device
     pg, px, ps = _rows("gate", gate, shape, dtype, dev), _rows("x", x, shape, dtype, dev), _state("h0", h0, (batch, D), dev)
-    h = torch.empty(shape, dtype=dtype, device=gate.device)
-    last = torch.empty((batch, D), dtype=torch.float32, device=gate.device)
-    status = _launch(_library().trsm_linrec_forward, dev, code, kind, batch, T, D, *pg, *px, *ps, po, h.data_ptr(),
+    h = _empty(shape, dtype=dtype, device=device)
+    last = _empty((batch, D), dtype=_f32, device=device)
+    status = _launch(_typed.trsm_linrec_forward, dev, code, kind, batch, T, D, *pg, *px, *ps, po, h.data_ptr(),
                      T * D, D, last.data_ptr())
     if status:
         _check("trsm_linrec_forward", status)
@@ -204,11 +211,12 @@ def linear_recurrence_backward(gate, x, h, dh, h0=None, dh_last=None, *, form="d
     """Gradients (dgate, dx, dh0) of ``linear_recurrence`` from ``h``, its
     output, and ``dh`` and ``dh_last``, the gradients of its two results
     (dh_last None: zero).  ``x`` may be None unless form is "sigmoid"."""
-    torch = _load_torch()
+    if _torch is None:
+        _load_torch()
     code, batch, T, D, dev, po = _gate(gate, offsets)
-    kind = _code(FORMS, form, "form")
-    shape, dtype = gate.shape, gate.dtype
-    pg, ph, pd = (_rows(name, t, shape, dtype, dev) for name, t in (("gate", gate), ("h", h), ("dh", dh)))
+    kind = FORMS[form] if form in FORMS else _code(FORMS, form, "form")
+    shape, dtype, device = gate.shape, gate.dtype, gate.device
+    pg, ph, pd = _rows("gate", gate, shape, dtype, dev), _rows("h", h, shape, dtype, dev), _rows("dh", dh, shape, dtype, dev)
     if x is not None:
         px = _rows("x", x, shape, dtype, dev)
     elif kind == FORMS["sigmoid"]:
@@ -220,10 +228,10 @@ def linear_recurrence_backward(gate, x, h, dh, h0=None, dh_last=None, *, form="d
     if pl and ld != D and batch > 1:
         dh_last = dh_last.contiguous()
         pl = dh_last.data_ptr()
-    dgate = torch.empty(shape, dtype=dtype, device=gate.device)
-    dx = torch.empty(shape, dtype=dtype, device=gate.device)
-    dh0 = torch.empty((batch, D), dtype=torch.float32, device=gate.device)
-    status = _launch(_library().trsm_linrec_backward, dev, code, kind, batch, T, D, *pg, *px, *ph, *ps, *pd, pl, po,
+    dgate = _empty(shape, dtype=dtype, device=device)
+    dx = _empty(shape, dtype=dtype, device=device)
+    dh0 = _empty((batch, D), dtype=_f32, device=device)
+    status = _launch(_typed.trsm_linrec_backward, dev, code, kind, batch, T, D, *pg, *px, *ph, *ps, *pd, pl, po,
                      dgate.data_ptr(), T * D, D, dx.data_ptr(), T * D, D, dh0.data_ptr())
     if status:
         _check("trsm_linrec_backward", status)
@@ -296,7 +304,8 @@ def linear_recurrence_step(gate, x, state, *, form="decay", slots=None, out_stat
     else in ``state`` itself.  A slot outside the table marks a row of
     padding: zero comes out and no state is touched.  Returns the new states
     as (batch, D) of gate's type."""
-    torch = _load_torch()
+    if _torch is None:
+        _load_torch()
     shape, dtype, dev = gate.shape, gate.dtype, gate.get_device()
     code = _elem.get(dtype)
     if dev < 0:
@@ -305,24 +314,24 @@ def linear_recurrence_step(gate, x, state, *, form="decay", slots=None, out_stat
         raise TypeError(f"gate: {dtype} (float32, float16 or bfloat16)")
     if len(shape) != 2:
         raise ValueError("gate: expected (batch, D)")
-    kind = _code(FORMS, form, "form")
+    kind = FORMS[form] if form in FORMS else _code(FORMS, form, "form")
     batch, D = shape
     pg, _, sg = _rows("gate", gate, shape, dtype, dev)
     px, _, sx = _rows("x", x, shape, dtype, dev)
-    if state.dim() != 2:
-        raise ValueError("state: expected (slots, D)")
-    table = (state.shape[0], D)
+    table = state.shape
+    if len(table) != 2 or table[1] != D:
+        raise ValueError(f"state: shape {tuple(table)}, expected (slots, {D})")
     ps, ss = _state("state", state, table, dev)
     pn, sn = (ps, ss) if out_state is None else _state("out_state", out_state, table, dev)
     pi = None
     if slots is not None:
-        if slots.dtype is not torch.int32 or slots.shape != (batch,) or (batch > 1 and slots.stride(0) != 1):
+        if slots.dtype is not _torch.int32 or slots.shape != (batch,) or (batch > 1 and slots.stride(0) != 1):
             raise ValueError("slots: a contiguous int32 vector of batch state numbers")
         if slots.get_device() != dev:
             raise ValueError(f"slots: on {slots.device}, expected {gate.device}")
         pi = slots.data_ptr()
-    y = torch.empty(shape, dtype=dtype, device=gate.device)
-    status = _launch(_library().trsm_linrec_step, dev, code, kind, batch, D, pg, sg, px, sx, pi, table[0], ps, ss, pn, sn,
+    y = _empty(shape, dtype=dtype, device=gate.device)
+    status = _launch(_typed.trsm_linrec_step, dev, code, kind, batch, D, pg, sg, px, sx, pi, table[0], ps, ss, pn, sn,
                      y.data_ptr(), D)
     if status:
         _check("trsm_linrec_step", status)
@@ -356,43 +365,50 @@ def orthogonalize(G, *, steps=5, coefficients=None, eps=1e-7, out=None):
     like G), or a new tensor: float16 for a float16 G, else bfloat16.
     """
     torch = _load_torch()
-    if not G.is_cuda:
+    code, shape, dev = _elem.get(G.dtype), G.shape, G.get_device()
+    if dev < 0:
         raise ValueError("orthogonalize takes CUDA (device) tensors; got a CPU tensor")
-    code = _elem.get(G.dtype)
     if code is None:
         raise TypeError(f"G: {G.dtype} (float32, float16 or bfloat16)")
-    if G.dim() not in (2, 3):
+    if len(shape) not in (2, 3):
         raise ValueError("G: expected (m, n) or (batch, m, n)")
     if not 0 <= steps <= 64:
         raise ValueError(f"steps: {steps} (0 to 64)")
-    if out is None:
-        out = torch.empty(G.shape, dtype=torch.float16 if code == 1 else torch.bfloat16, device=G.device)
-        if G.numel() and _matrices("G", G)[2]:
-            out = torch.empty(G.mT.shape, dtype=out.dtype, device=G.device).mT
-    else:
-        if out.shape != G.shape:
-            raise ValueError(f"out: shape {tuple(out.shape)}, expected {tuple(G.shape)}")
-        if out.dtype not in (torch.float16, torch.bfloat16):
-            raise TypeError(f"out: {out.dtype} (float16 or bfloat16)")
-        if out.get_device() != G.get_device():
-            raise ValueError(f"out: on {out.device}, expected {G.device}")
+    m, n = shape[-2], shape[-1]
+    batch = shape[0] if len(shape) == 3 else 1
     coef = _coefficients(steps, coefficients)
-    if not G.numel():
+    some = m and n and batch
+    ldg, sg, flip = _matrices("G", G) if some else (n, 0, False)
+    if out is None:
+        out_code = 1 if code == 1 else 2
+        dtype = torch.float16 if code == 1 else torch.bfloat16
+        if flip:
+            out = _empty((*shape[:-2], n, m), dtype=dtype, device=G.device).mT
+            ldo, so = m, m * n
+        else:
+            out = _empty(shape, dtype=dtype, device=G.device)
+            ldo, so = n, m * n
+    else:
+        if out.shape != shape:
+            raise ValueError(f"out: shape {tuple(out.shape)}, expected {tuple(shape)}")
+        out_code = _elem.get(out.dtype)
+        if out_code not in (1, 2):
+            raise TypeError(f"out: {out.dtype} (float16 or bfloat16)")
+        if out.get_device() != dev:
+            raise ValueError(f"out: on {out.device}, expected {G.device}")
+        if some:
+            ldo, so, flip_out = _matrices("out", out)
+            if flip != flip_out:
+                # a single row or column may be either
+                if min(m, n) > 1 or any(not t.is_contiguous() for t in (G, out)):
+                    raise ValueError("out: must be row-major where G is, and column-major where G is")
+                flip, ldg, ldo = False, n, n
+    if not some:
         return out
-    ldg, sg, flip = _matrices("G", G)
-    ldo, so, flip_out = _matrices("out", out)
-    m, n = G.shape[-2:]
-    if flip != flip_out:
-        if min(m, n) > 1:
-            raise ValueError("out: must be row-major where G is, and column-major where G is")
-        flip, ldg, ldo = False, n, n  # a single row or column is both
-        if any(t.shape[-1] > 1 and t.stride(-1) != 1 or t.shape[-2] > 1 and t.stride(-2) != n for t in (G, out)):
-            raise ValueError("out: must be row-major where G is, and column-major where G is")
     if flip:
         m, n = n, m
-    batch = G.shape[0] if G.dim() == 3 else 1
-    status = _launch(_library().trsm_orthogonalize, G.get_device(), code, _elem[out.dtype], m, n, G.data_ptr(), ldg, sg,
-                     out.data_ptr(), ldo, so, batch, steps, coef, eps, None, 0)
+    status = _launch(_typed.trsm_orthogonalize, dev, code, out_code, m, n, G.data_ptr(), ldg, sg, out.data_ptr(),
+                     ldo, so, batch, steps, coef, eps, None, 0)
     if status:
         _check("trsm_orthogonalize", status)
     return out
