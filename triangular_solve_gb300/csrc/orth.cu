@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const Input in, doub
             next();
         }
     }
-    const double t = block_sum(s.total());
+    const double t = block_sum(s);
     if (threadIdx.x == 0) partial[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = t;
 }
 

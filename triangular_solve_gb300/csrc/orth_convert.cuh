@@ -51,11 +51,23 @@ struct Squares {
     }
 };
 
-// Sum over a block's threads, in a fixed order; valid in thread 0.
-__device__ __forceinline__ double block_sum(double v) {
+// Sum of squares of a block's threads, in a fixed order; valid in thread 0.
+// In single precision (at most 10 roundings of sums of positive terms) unless
+// some thread met values out of the ordinary.
+__device__ __forceinline__ double block_sum(const Squares &s) {
     __shared__ double part[32];
+    const bool wide = __syncthreads_or(s.big != 0.f || s.small != 0.f || !(s.mid < 0x1p90f));
+    double v;
+    if (!wide) {
+        float f = s.mid;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_down_sync(~0u, v, o);
+        for (int o = 16; o; o >>= 1) f += __shfl_down_sync(~0u, f, o);
+        v = f;
+    } else {
+        v = s.total();
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v += __shfl_down_sync(~0u, v, o);
+    }
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     if (threadIdx.x == 0)
@@ -82,13 +94,25 @@ constexpr int kMaxSteps = 64;
 struct Scale {
     float up, more, rho;  // 2^e = up * more, neither of which overflows
 };
+// (Double precision takes care of the range alone: its root and quotient are
+// a microsecond on this GPU.)
 __device__ __forceinline__ Scale scale_from(double sum_of_squares, double eps) {
-    const double s = 1.0 / (sqrt(sum_of_squares) + eps);
-    if (!(s > 0 && s < 1e300)) return {1.f, 1.f, __int_as_float(0x7fffffff)};
-    int e = ilogb(s);
-    const float rho = (float)scalbn(s, -e);
-    e = min(max(e, -160), 240);
-    return {scalbnf(1.f, e / 2), scalbnf(1.f, e - e / 2), rho};
+    const Scale none = {1.f, 1.f, __int_as_float(0x7fffffff)};
+    if (sum_of_squares > 1e-30 && sum_of_squares < 1e30 && eps < 1e15) {  // within single precision
+        const float s = 1.f / (sqrtf((float)sum_of_squares) + (float)eps);
+        const int e = ((__float_as_int(s) >> 23) & 255) - 127;
+        const float up = __int_as_float((e + 127) << 23);
+        return {up, 1.f, s / up};
+    }
+    if (!(sum_of_squares >= 0 && sum_of_squares < 1e300)) return none;
+    // |G| + eps = t 2^h, h chosen by the larger of the two
+    const int hs = sum_of_squares > 0 ? ilogb(sum_of_squares) >> 1 : -2000, he = eps > 0 ? ilogb(eps) : -2000;
+    const int h = max(hs, he);
+    if (h == -2000) return none;
+    const float t = sqrtf((float)scalbn(sum_of_squares, -2 * h)) + (float)scalbn(eps, -h);
+    const float s = 1.f / t;  // t is in [1, 4)
+    const int es = ilogbf(s), e = min(max(es - h, -160), 240);
+    return {scalbnf(1.f, e / 2), scalbnf(1.f, e - e / 2), scalbnf(s, -es)};
 }
 // The same from a matrix's partial sums, by a whole block; every thread gets
 // the same.

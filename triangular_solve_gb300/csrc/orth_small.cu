@@ -22,8 +22,6 @@
 namespace trsm {
 namespace orth {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-
 struct SmallArgs {
     Input in;
     int r, c, cp, ldx;  // c rounded up to 16; row length of X in shared memory
@@ -58,11 +56,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
 
 // Tiles of the R x R products: WM x WN for each warp, the K dimension of
 // X X^T cut between the warps where there are fewer tiles than warps.
-template <int R> struct SmallShape {
-    static constexpr int WM = R == 128 ? 32 : 16, WN = R == 128 ? 64 : 32;
-    static constexpr int kTiles = (R / WM) * (R / WN), kCut = kWarps / kTiles;
+template <int R, int WARPS> struct SmallShape {
+    static constexpr int WM = R == 128 ? 32 : 16, WN = R == 32 ? 32 : R == 128 ? 64 : 512 / (2 * WARPS);
+    static constexpr int kTiles = (R / WM) * (R / WN), kCut = WARPS / kTiles;
+    static_assert(kTiles * kCut == WARPS, "a tile for each warp");
     static constexpr int ld = R + 8;  // of S and C: rows 16 bytes apart in the banks
-    static constexpr size_t kScratch = kCut > 1 ? (size_t)kWarps * WM * WN * 4 : 0;
+    static constexpr size_t kScratch = kCut > 1 ? (size_t)WARPS * WM * WN * 4 : 0;
+    // CTAs an SM should hold
+    static constexpr int kBlocks = R == 128 ? 2 : 24 / WARPS;
     static size_t smem(int ldx, bool tail) {
         return (size_t)R * ldx * 2 * (tail ? 2 : 1) + 2 * (size_t)R * ld * 2 + kScratch;
     }
@@ -90,10 +91,11 @@ __device__ __forceinline__ void tile_product(float (&acc)[WM / 16][WN / 8][4], u
     }
 }
 
-template <typename T, int R>
-__global__ void __launch_bounds__(kThreads) small_kernel(const __grid_constant__ SmallArgs g) {
-    using W = SmallShape<R>;
-    constexpr int WM = W::WM, WN = W::WN;
+template <typename T, int R, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, SmallShape<R, WARPS>::kBlocks)
+    small_kernel(const __grid_constant__ SmallArgs g) {
+    using W = SmallShape<R, WARPS>;
+    constexpr int WM = W::WM, WN = W::WN, kWarps = WARPS, kThreads = 32 * WARPS;
     extern __shared__ __align__(16) unsigned char small_smem[];
     __half *const Xh = reinterpret_cast<__half *>(small_smem);
     __half *const Xl = Xh + (size_t)R * g.ldx;
@@ -106,25 +108,34 @@ __global__ void __launch_bounds__(kThreads) small_kernel(const __grid_constant__
     const T *G = static_cast<const T *>(g.in.G) + z * g.in.stride;
     const int m = (int)g.in.m, n = (int)g.in.n, per = (n + 7) / 8;
 
-    // |G|_F, while X is set to zero (its padding stays so)
+    // |G|_F, while X is set to zero (its padding stays so).  The first kHeld
+    // groups of a thread stay in registers for X_0, the rest is read again.
+    constexpr int kHeld = 2;
+    float held[kHeld][8];
     Squares sq;
-    for (int e = tid; e < m * per; e += kThreads) {
+#pragma unroll
+    for (int q = 0; q < kHeld; ++q) {
+        const int e = tid + q * kThreads;
+        if (e < m * per) load_8<T>(G + (int64_t)(e / per) * g.in.ld, e % per * 8, n, g.in.vec, held[q]);
+    }
+    for (int e = tid; e < R * g.ldx * (g.any_tail ? 2 : 1) / 8; e += kThreads)
+        reinterpret_cast<uint4 *>(Xh)[e] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int q = 0; q < kHeld; ++q)
+        if (tid + q * kThreads < m * per) sq.add_8(held[q]);
+    for (int e = tid + kHeld * kThreads; e < m * per; e += kThreads) {
         float v[8];
         load_8<T>(G + (int64_t)(e / per) * g.in.ld, e % per * 8, n, g.in.vec, v);
         sq.add_8(v);
     }
-    for (int e = tid; e < R * g.ldx * (g.any_tail ? 2 : 1) / 8; e += kThreads)
-        reinterpret_cast<uint4 *>(Xh)[e] = make_uint4(0, 0, 0, 0);
-    const double sum = block_sum(sq.total());
+    const double sum = block_sum(sq);
     if (tid == 0) scale = scale_from(sum, g.eps);
     __syncthreads();
     const float rho = scale.rho;
 
     // X_0
-    for (int e = tid; e < m * per; e += kThreads) {
+    auto put = [&](int e, const float (&v)[8]) {
         const int i = e / per, j = e % per * 8;
-        float v[8];
-        load_8<T>(G + (int64_t)i * g.in.ld, j, n, g.in.vec, v);
         alignas(16) __half hi[8], lo[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) split(v[k] * scale.up * scale.more * kScaleX, hi[k], lo[k]);
@@ -140,6 +151,14 @@ __global__ void __launch_bounds__(kThreads) small_kernel(const __grid_constant__
                 }
             }
         }
+    };
+#pragma unroll
+    for (int q = 0; q < kHeld; ++q)
+        if (tid + q * kThreads < m * per) put(tid + q * kThreads, held[q]);
+    for (int e = tid + kHeld * kThreads; e < m * per; e += kThreads) {
+        float v[8];
+        load_8<T>(G + (int64_t)(e / per) * g.in.ld, e % per * 8, n, g.in.vec, v);
+        put(e, v);
     }
     __syncthreads();
 
@@ -212,51 +231,67 @@ __global__ void __launch_bounds__(kThreads) small_kernel(const __grid_constant__
         }
         __syncthreads();
         // X = C X in place: a warp holds 16 columns of X in registers and
-        // writes them anew row tile by row tile
+        // writes them anew, two row tiles at a time (their sums are what there
+        // is to do in parallel).  Where there are fewer strips of columns than
+        // warps, several warps hold a strip and share its rows.
         float alpha = (s == 0 ? rho : 1.f) / kScaleS;
         if (last) alpha /= kScaleX;
-        for (int j0 = 16 * warp; j0 < g.cp; j0 += 16 * kWarps) {
-            uint32_t bh[R / 16][4], bl[R / 16][4];
+        constexpr int kRowTiles = R / 16, kAtOnce = R == 128 ? 1 : 2;
+        const int strips = g.cp / 16;
+        const int share = 2 * strips > kWarps ? 1 : min(kWarps / strips, kRowTiles / kAtOnce);
+        for (int strip = warp / share; strip < strips || share > 1; strip += kWarps) {
+            uint32_t bh[kRowTiles][4], bl[kRowTiles][4];
+            const int j0 = 16 * min(strip, strips - 1);
             const uint32_t at = 2 * ((lane & 15) * g.ldx + j0 + (lane >> 4) * 8);
 #pragma unroll
-            for (int k = 0; k < R / 16; ++k) ldmatrix4_trans(bh[k], xh + at + 2 * 16 * k * g.ldx);
+            for (int k = 0; k < kRowTiles; ++k) ldmatrix4_trans(bh[k], xh + at + 2 * 16 * k * g.ldx);
             if (split_x) {
 #pragma unroll
-                for (int k = 0; k < R / 16; ++k) ldmatrix4_trans(bl[k], xl + at + 2 * 16 * k * g.ldx);
+                for (int k = 0; k < kRowTiles; ++k) ldmatrix4_trans(bl[k], xl + at + 2 * 16 * k * g.ldx);
             }
-            __syncwarp();
+            if (share > 1) __syncthreads();  // each warp has one strip at most
+            else __syncwarp();
+            if (strip >= strips) break;
 #pragma unroll 1
-            for (int i = 0; i < R / 16; ++i) {
-                float acc[2][4] = {};
+            for (int i = kAtOnce * (warp % share); i < kRowTiles; i += kAtOnce * share) {
+                float acc[kAtOnce][2][4] = {};
                 const uint32_t pa = sC + 2 * ((16 * i + (lane & 15)) * W::ld + (lane >> 4) * 8);
 #pragma unroll
-                for (int k = 0; k < R / 16; ++k) {
-                    uint32_t a[4];
-                    ldmatrix4(a, pa + 2 * 16 * k);
-                    mma_f16(acc[0], a, bh[k][0], bh[k][1]);
-                    mma_f16(acc[1], a, bh[k][2], bh[k][3]);
+                for (int k = 0; k < kRowTiles; ++k) {
+                    uint32_t a[kAtOnce][4];
+#pragma unroll
+                    for (int t = 0; t < kAtOnce; ++t) ldmatrix4(a[t], pa + 2 * (16 * t * W::ld + 16 * k));
+#pragma unroll
+                    for (int t = 0; t < kAtOnce; ++t)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) mma_f16(acc[t][j], a[t], bh[k][2 * j], bh[k][2 * j + 1]);
                     if (split_x) {
-                        mma_f16(acc[0], a, bl[k][0], bl[k][1]);
-                        mma_f16(acc[1], a, bl[k][2], bl[k][3]);
+#pragma unroll
+                        for (int t = 0; t < kAtOnce; ++t)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) mma_f16(acc[t][j], a[t], bl[k][2 * j], bl[k][2 * j + 1]);
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int t = 0; t < kAtOnce; ++t)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int p = (16 * i + row + 8 * h) * g.ldx + j0 + 8 * j + col;
-                        const float o0 = alpha * acc[j][2 * h], o1 = alpha * acc[j][2 * h + 1];
-                        if (last && g.bf16) {  // the result's bits, in X's place
-                            *reinterpret_cast<__nv_bfloat162 *>(Xh + p) = __floats2bfloat162_rn(o0, o1);
-                        } else {
-                            const __half2 hi = __floats2half2_rn(o0, o1);
-                            *reinterpret_cast<__half2 *>(Xh + p) = hi;
-                            if (split_next)
-                                *reinterpret_cast<__half2 *>(Xl + p) =
-                                    __floats2half2_rn(o0 - __low2float(hi), o1 - __high2float(hi));
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int p = (16 * (i + t) + row + 8 * h) * g.ldx + j0 + 8 * j + col;
+                            const float o0 = alpha * acc[t][j][2 * h], o1 = alpha * acc[t][j][2 * h + 1];
+                            if (last && g.bf16) {  // the result's bits, in X's place
+                                *reinterpret_cast<__nv_bfloat162 *>(Xh + p) = __floats2bfloat162_rn(o0, o1);
+                            } else {
+                                const __half2 hi = __floats2half2_rn(o0, o1);
+                                *reinterpret_cast<__half2 *>(Xh + p) = hi;
+                                if (split_next)
+                                    *reinterpret_cast<__half2 *>(Xl + p) =
+                                        __floats2half2_rn(o0 - __low2float(hi), o1 - __high2float(hi));
+                            }
                         }
-                    }
             }
+            if (share > 1) break;
         }
         __syncthreads();
     }
@@ -286,7 +321,7 @@ constexpr size_t kMostSmem = 224 * 1024;
 // With a tail, which the coefficients may ask for or not: whether a call
 // needs a workspace depends on the shape alone.
 template <int R> bool fits(int64_t c) {
-    return SmallShape<R>::smem((int)((c + 15) / 16 * 16 + 8), true) <= kMostSmem;
+    return SmallShape<R, 8>::smem((int)((c + 15) / 16 * 16 + 8), true) <= kMostSmem;
 }
 // Rows of the kernel that takes r x c matrices, or 0.
 int small_rows(int64_t r, int64_t c) {
@@ -297,17 +332,22 @@ int small_rows(int64_t r, int64_t c) {
     return 0;
 }
 
-template <typename T, int R> int launch(const SmallArgs &g, int64_t batch, cudaStream_t st) {
-    const size_t smem = SmallShape<R>::smem(g.ldx, g.any_tail);
-    const cudaError_t e = cudaFuncSetAttribute(small_kernel<T, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+template <typename T, int R, int WARPS> int launch(const SmallArgs &g, int64_t batch, cudaStream_t st) {
+    const size_t smem = SmallShape<R, WARPS>::smem(g.ldx, g.any_tail);
+    const cudaError_t e = cudaFuncSetAttribute(small_kernel<T, R, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)kMostSmem);
     if (e != cudaSuccess) return cuda_status(e);
-    small_kernel<T, R><<<(unsigned)batch, kThreads, smem, st>>>(g);
+    small_kernel<T, R, WARPS><<<(unsigned)batch, 32 * WARPS, smem, st>>>(g);
     return launch_status();
 }
 template <typename T> int launch_rows(const SmallArgs &g, int rows, int64_t batch, cudaStream_t st) {
-    return rows == 32 ? launch<T, 32>(g, batch, st) : rows == 64 ? launch<T, 64>(g, batch, st)
-                                                                 : launch<T, 128>(g, batch, st);
+    if (rows == 128) return launch<T, 128, 8>(g, batch, st);
+    // four warps keep more of the smallest matrices on an SM (512 of 32 x 32: 15
+    // us, with eight 24; 1024 of 64 x 64: 49, 53), eight finish larger ones
+    // sooner (300 of 64 x 128: 28, with four 32; 1 of 64 x 800: 76, 105)
+    const bool four = rows * g.c <= 4096;
+    if (rows == 64) return four ? launch<T, 64, 4>(g, batch, st) : launch<T, 64, 8>(g, batch, st);
+    return four ? launch<T, 32, 4>(g, batch, st) : launch<T, 32, 8>(g, batch, st);
 }
 
 }  // namespace orth
