@@ -516,3 +516,48 @@ def test_expired_wait_is_reported_and_leaves_the_device_usable(env):
         tg.trsm_set_wait_limit(-1)
     h, l2 = tg.linear_recurrence(g, x)
     assert torch.equal(h, want) and torch.equal(l2, last) and tg.trsm_device_status() == 0
+
+
+def test_marshalled_calls_equal_the_python_ones(env, monkeypatch):
+    """The calls' C half takes plain calls and leaves everything else to the
+    Python half, with the same results."""
+    import sysconfig
+    import os
+    torch, tg = env
+    from triangular_solve_gb300 import model
+    model._load_torch()
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        pytest.skip("Python's headers are not here")
+    m = model._marshal
+    assert m is not None
+    gen = torch.Generator("cuda").manual_seed(1)
+
+    def rnd(*s, dtype=torch.bfloat16):
+        return torch.randn(s, generator=gen, device="cuda").to(dtype)
+
+    both = rnd(3, 40, 64)
+    g, x = both[..., :32], both[..., 32:]
+    h0, dl = rnd(3, 32, dtype=torch.float32), rnd(3, 32, dtype=torch.float32)
+    off = torch.tensor([0, 3, 40], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([4, 0, 2], dtype=torch.int32, device="cuda")
+    table = rnd(5, 32, dtype=torch.float32)
+
+    def calls(out):
+        h, last = tg.linear_recurrence(g, x, h0, form="sigmoid")
+        r = [h, last, *tg.linear_recurrence(g[0], x[0], form="decay", offsets=off)]
+        r += tg.linear_recurrence_backward(g, x, h, x, h0, dl, form="sigmoid")
+        r += tg.linear_recurrence_backward(g[0], None, h[0], x[0], offsets=off)
+        return r + [tg.linear_recurrence_step(g[:, 0], x[:, 0], table, form="log", slots=slots, out_state=out), out]
+
+    assert m.forward(g, x, h0, "sigmoid", None) is not None
+    fast = calls(torch.zeros_like(table))
+    monkeypatch.setattr(model, "_marshal", None)
+    slow = calls(torch.zeros_like(table))
+    assert len(fast) == len(slow) and all(torch.equal(a, b) for a, b in zip(fast, slow))
+    for bad in ((g.cpu(), x, None, "decay", None), (g, x.float(), None, "decay", None), (g, x, h0[:2], "decay", None),
+                (g, x, None, "tanh", None), (g[0], x[0], None, "decay", None), (g, x, None, 0, None),
+                (g.transpose(1, 2), x, None, "decay", None), (None, x, None, "decay", None), (g, x, None, "decay", off)):
+        assert m.forward(*bad) is None
+    assert m.step(g[:, 0], x[:, 0], table, "log", slots[:2], None) is None
+    assert m.step(g[:, 0], x[:, 0], table[:, :8], "log", slots, None) is None
+    assert m.backward(g, None, g, x, None, None, "sigmoid", None) is None

@@ -14,11 +14,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libtrsm_gb300.so")
+MARSHAL = os.path.join(BUILD, "_marshal.so")  # a Python extension, see csrc/marshal.c
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -48,6 +50,25 @@ def _compile(src: str, obj: str, extra: list[str]) -> tuple[str, str]:
     return src, r.stderr
 
 
+def _build_marshal(force: bool) -> None:
+    """The C half of the Python binding.  It needs Python's headers; without them
+    the binding does all of its work in Python."""
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        return
+    src = os.path.join(CSRC, "marshal.c")
+    newest = max(os.path.getmtime(p) for p in [src, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
+        return
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-fPIC", "-shared", "-I", INCLUDE, "-I", include, src, "-o", tmp,
+           "-L", BUILD, "-l:libtrsm_gb300.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on marshal.c:\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -75,6 +96,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(tmp, LIB)
+    _build_marshal(force)
     if verbose_ptxas:
         print("\n".join(logs))
     return LIB

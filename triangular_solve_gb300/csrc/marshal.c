@@ -1,0 +1,304 @@
+/*
+ * The recurrence's Python calls, marshalled in C: a small call's time is
+ * mostly that of reading its tensors' attributes in Python (step of one
+ * request: 12 us from Python, 6 from here, 2 of them the launch).
+ *
+ * Each function takes the arguments of its namesake in model.py and returns
+ * the results, or the library's status as an int where that is not zero, or
+ * None for anything but plain valid arguments on the current device, which
+ * model.py then handles or refuses itself.  Nothing here raises for an
+ * argument.
+ */
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include "trsm_model.h"
+
+static PyObject *g_empty, *g_dtypes[3], *g_i32, *g_get_device, *g_get_stream, *g_forms[3];
+static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device, *s_device, *s_empty_kw;
+
+typedef struct {
+    PyObject *dtype; /* borrowed from torch, which keeps its dtypes */
+    int dims;
+    int64_t shape[3], stride[3];
+    void *p;
+    long device;
+} Tensor;
+
+static int read_tuple(PyObject *t, int64_t *out, int *n) {
+    if (!t || !PyTuple_Check(t) || PyTuple_GET_SIZE(t) > 3) return 0;
+    *n = (int)PyTuple_GET_SIZE(t);
+    for (int i = 0; i < *n; ++i) {
+        out[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(t, i));
+        if (out[i] == -1 && PyErr_Occurred()) return 0;
+    }
+    return 1;
+}
+
+/* 1, or 0 where it is no tensor of at most three dimensions (no error is left set). */
+static int read_tensor(PyObject *t, Tensor *o) {
+    int ok = 0, n = 0;
+    PyObject *v = PyObject_GetAttr(t, s_dtype);
+    if (!v) goto done;
+    o->dtype = v;
+    Py_DECREF(v);
+    v = PyObject_GetAttr(t, s_shape);
+    ok = read_tuple(v, o->shape, &o->dims);
+    Py_XDECREF(v);
+    if (!ok) goto done;
+    v = PyObject_CallMethodNoArgs(t, s_stride);
+    ok = read_tuple(v, o->stride, &n) && n == o->dims;
+    Py_XDECREF(v);
+    if (!ok) goto done;
+    v = PyObject_CallMethodNoArgs(t, s_get_device);
+    o->device = v ? PyLong_AsLong(v) : -1;
+    Py_XDECREF(v);
+    v = PyObject_CallMethodNoArgs(t, s_data_ptr);
+    o->p = v ? PyLong_AsVoidPtr(v) : NULL;
+    ok = v != NULL;
+    Py_XDECREF(v);
+done:
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        return 0;
+    }
+    return ok;
+}
+
+/* A tensor of the gate's shape, type and device with contiguous channels. */
+static int like(PyObject *t, const Tensor *g, Tensor *o) {
+    if (!read_tensor(t, o) || o->dtype != g->dtype || o->device != g->device || o->dims != g->dims) return 0;
+    for (int i = 0; i < o->dims; ++i)
+        if (o->shape[i] != g->shape[i]) return 0;
+    return o->stride[o->dims - 1] == 1;
+}
+/* Float states of `rows` (any number: -1) x D, or None. */
+static int states(PyObject *t, const Tensor *g, int64_t rows, int64_t D, Tensor *o) {
+    o->p = NULL;
+    o->stride[0] = 0;
+    o->shape[0] = 0;
+    if (t == Py_None) return 1;
+    return read_tensor(t, o) && o->dtype == g_dtypes[0] && o->device == g->device && o->dims == 2 &&
+           (rows < 0 || o->shape[0] == rows) && o->shape[1] == D && o->stride[1] == 1;
+}
+static int indices(PyObject *t, const Tensor *g, Tensor *o) {
+    o->p = NULL;
+    if (t == Py_None) return 1;
+    return read_tensor(t, o) && o->dtype == g_i32 && o->device == g->device && o->dims == 1 && o->shape[0] > 0 &&
+           o->stride[0] == 1;
+}
+static int elem_of(const Tensor *t) {
+    for (int i = 0; i < 3; ++i)
+        if (t->dtype == g_dtypes[i]) return i;
+    return -1;
+}
+static int form_of(PyObject *f) {
+    for (int i = 0; i < 3; ++i)
+        if (f == g_forms[i]) return i;
+    for (int i = 0; i < 3; ++i)
+        if (PyUnicode_Check(f) && PyUnicode_Compare(f, g_forms[i]) == 0) return i;
+    return -1;
+}
+/* The current stream of the gate's device, if that is the current device. */
+static int stream_of(const Tensor *g, void **stream) {
+    PyObject *v = PyObject_CallNoArgs(g_get_device);
+    const long dev = v ? PyLong_AsLong(v) : -1;
+    Py_XDECREF(v);
+    int ok = dev >= 0 && dev == g->device;
+    if (ok) {
+        PyObject *d = PyLong_FromLong(dev);
+        v = d ? PyObject_CallOneArg(g_get_stream, d) : NULL;
+        Py_XDECREF(d);
+        *stream = v ? PyLong_AsVoidPtr(v) : NULL;
+        ok = v != NULL;
+        Py_XDECREF(v);
+    }
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        return 0;
+    }
+    return ok;
+}
+/* torch.empty(shape, dtype=..., device=...); *p its memory.  An exception (out
+ * of memory) stays set. */
+static PyObject *empty(PyObject *shape, PyObject *dtype, PyObject *device, void **p) {
+    PyObject *args[3] = {shape, dtype, device};
+    PyObject *t = PyObject_Vectorcall(g_empty, args, 1, s_empty_kw);
+    if (!t) return NULL;
+    PyObject *v = PyObject_CallMethodNoArgs(t, s_data_ptr);
+    *p = v ? PyLong_AsVoidPtr(v) : NULL;
+    Py_XDECREF(v);
+    if (!v || PyErr_Occurred()) {
+        Py_DECREF(t);
+        return NULL;
+    }
+    return t;
+}
+
+/* Geometry of the gate and its sequences. */
+typedef struct {
+    Tensor gate, offsets;
+    int elem, form;
+    int64_t batch, T, D;
+    void *stream;
+} Call;
+static int read_call(PyObject *gate, PyObject *form, PyObject *offsets, Call *c) {
+    if (!read_tensor(gate, &c->gate) || c->gate.device < 0 || c->gate.dims < 1) return 0;
+    const Tensor *g = &c->gate;
+    c->elem = elem_of(g);
+    c->form = form_of(form);
+    if (c->elem < 0 || c->form < 0 || g->stride[g->dims - 1] != 1 || !indices(offsets, g, &c->offsets)) return 0;
+    if (offsets == Py_None) {
+        if (g->dims != 3) return 0;
+        c->batch = g->shape[0], c->T = g->shape[1], c->D = g->shape[2];
+    } else {
+        if (g->dims != 2) return 0;
+        c->batch = c->offsets.shape[0] - 1, c->T = g->shape[0], c->D = g->shape[1];
+    }
+    return c->batch > 0 && c->T > 0 && c->D > 0 && stream_of(g, &c->stream);
+}
+#define STRIDE_B(t) ((t).dims == 3 ? (t).stride[0] : 0)
+#define STRIDE_T(t) ((t).dims == 3 ? (t).stride[1] : (t).stride[0])
+#define ROWS(t) (t).p, STRIDE_B(t), STRIDE_T(t)
+
+/* (gate, x, h0, form, offsets) */
+static PyObject *forward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    Call c;
+    Tensor x, h0;
+    if (n != 5 || !read_call(a[0], a[3], a[4], &c) || !like(a[1], &c.gate, &x) ||
+        !states(a[2], &c.gate, c.batch, c.D, &h0))
+        Py_RETURN_NONE;
+    void *ph, *pl;
+    PyObject *h = NULL, *last = NULL, *out = NULL;
+    PyObject *shape = PyObject_GetAttr(a[0], s_shape), *device = PyObject_GetAttr(a[0], s_device);
+    PyObject *small = Py_BuildValue("(LL)", (long long)c.batch, (long long)c.D);
+    if (shape && device && small) h = empty(shape, c.gate.dtype, device, &ph);
+    if (h) last = empty(small, g_dtypes[0], device, &pl);
+    if (last) {
+        int rc;
+        Py_BEGIN_ALLOW_THREADS;
+        rc = trsm_linrec_forward((trsm_elem_t)c.elem, (trsm_gate_t)c.form, c.batch, c.T, c.D, ROWS(c.gate), ROWS(x), h0.p,
+                                 h0.stride[0], c.offsets.p, ph, c.T * c.D, c.D, pl, c.stream);
+        Py_END_ALLOW_THREADS;
+        out = rc ? PyLong_FromLong(rc) : PyTuple_Pack(2, h, last);
+    }
+    Py_XDECREF(shape);
+    Py_XDECREF(device);
+    Py_XDECREF(small);
+    Py_XDECREF(h);
+    Py_XDECREF(last);
+    return out;
+}
+
+/* (gate, x, h, dh, h0, dh_last, form, offsets) */
+static PyObject *backward(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    Call c;
+    Tensor x, h, dh, h0, dl;
+    if (n != 8 || !read_call(a[0], a[6], a[7], &c) || !like(a[2], &c.gate, &h) || !like(a[3], &c.gate, &dh) ||
+        !states(a[4], &c.gate, c.batch, c.D, &h0) || !states(a[5], &c.gate, c.batch, c.D, &dl))
+        Py_RETURN_NONE;
+    if (dl.p && dl.stride[0] != c.D && c.batch > 1) Py_RETURN_NONE;
+    if (a[1] == Py_None && c.form != TRSM_GATE_SIGMOID) {
+        x = c.gate;
+        x.p = NULL;
+    } else if (!like(a[1], &c.gate, &x)) {
+        Py_RETURN_NONE;
+    }
+    void *pg, *px, *p0;
+    PyObject *dgate = NULL, *dx = NULL, *dh0 = NULL, *out = NULL;
+    PyObject *shape = PyObject_GetAttr(a[0], s_shape), *device = PyObject_GetAttr(a[0], s_device);
+    PyObject *small = Py_BuildValue("(LL)", (long long)c.batch, (long long)c.D);
+    if (shape && device && small) dgate = empty(shape, c.gate.dtype, device, &pg);
+    if (dgate) dx = empty(shape, c.gate.dtype, device, &px);
+    if (dx) dh0 = empty(small, g_dtypes[0], device, &p0);
+    if (dh0) {
+        int rc;
+        Py_BEGIN_ALLOW_THREADS;
+        rc = trsm_linrec_backward((trsm_elem_t)c.elem, (trsm_gate_t)c.form, c.batch, c.T, c.D, ROWS(c.gate), ROWS(x),
+                                  ROWS(h), h0.p, h0.stride[0], ROWS(dh), dl.p, c.offsets.p, pg, c.T * c.D, c.D, px,
+                                  c.T * c.D, c.D, p0, c.stream);
+        Py_END_ALLOW_THREADS;
+        out = rc ? PyLong_FromLong(rc) : PyTuple_Pack(3, dgate, dx, dh0);
+    }
+    Py_XDECREF(shape);
+    Py_XDECREF(device);
+    Py_XDECREF(small);
+    Py_XDECREF(dgate);
+    Py_XDECREF(dx);
+    Py_XDECREF(dh0);
+    return out;
+}
+
+/* (gate, x, state, form, slots, out_state) */
+static PyObject *step(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    Tensor g, x, state, next, slots;
+    void *stream, *py;
+    if (n != 6 || !read_tensor(a[0], &g) || g.device < 0 || g.dims != 2 || g.shape[0] < 1 || g.shape[1] < 1 ||
+        g.stride[1] != 1)
+        Py_RETURN_NONE;
+    const int elem = elem_of(&g), form = form_of(a[3]);
+    const int64_t batch = g.shape[0], D = g.shape[1];
+    if (elem < 0 || form < 0 || !like(a[1], &g, &x) || a[2] == Py_None || !states(a[2], &g, -1, D, &state) ||
+        !indices(a[4], &g, &slots) || (slots.p && slots.shape[0] != batch) || !stream_of(&g, &stream))
+        Py_RETURN_NONE;
+    if (a[5] == Py_None) next = state;
+    else if (!states(a[5], &g, state.shape[0], D, &next)) Py_RETURN_NONE;
+    PyObject *shape = PyObject_GetAttr(a[0], s_shape), *device = PyObject_GetAttr(a[0], s_device);
+    PyObject *y = shape && device ? empty(shape, g.dtype, device, &py) : NULL;
+    Py_XDECREF(shape);
+    Py_XDECREF(device);
+    if (!y) return NULL;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS;
+    rc = trsm_linrec_step((trsm_elem_t)elem, (trsm_gate_t)form, batch, D, g.p, g.stride[0], x.p, x.stride[0], slots.p,
+                          state.shape[0], state.p, state.stride[0], next.p, next.stride[0], py, D, stream);
+    Py_END_ALLOW_THREADS;
+    if (!rc) return y;
+    Py_DECREF(y);
+    return PyLong_FromLong(rc);
+}
+
+/* (torch, form names in the order of trsm_gate_t) */
+static PyObject *setup(PyObject *self, PyObject *args) {
+    PyObject *torch, *forms;
+    if (!PyArg_ParseTuple(args, "OO!", &torch, &PyTuple_Type, &forms)) return NULL;
+    static const char *const kDtypes[3] = {"float32", "float16", "bfloat16"};
+    for (int i = 0; i < 3; ++i) {
+        if (!(g_dtypes[i] = PyObject_GetAttrString(torch, kDtypes[i]))) return NULL;
+        PyObject *f = PyTuple_GetItem(forms, i);
+        if (!f) return NULL;
+        Py_INCREF(f);
+        PyUnicode_InternInPlace(&f);
+        g_forms[i] = f;
+    }
+    PyObject *c = PyObject_GetAttrString(torch, "_C");
+    if (!c) return NULL;
+    g_i32 = PyObject_GetAttrString(torch, "int32");
+    g_empty = PyObject_GetAttrString(torch, "empty");
+    g_get_device = PyObject_GetAttrString(c, "_cuda_getDevice");
+    g_get_stream = PyObject_GetAttrString(c, "_cuda_getCurrentRawStream");
+    Py_DECREF(c);
+    if (!g_i32 || !g_empty || !g_get_device || !g_get_stream) return NULL;
+    Py_RETURN_NONE;
+}
+
+static PyMethodDef methods[] = {
+    {"setup", setup, METH_VARARGS, NULL},
+    {"forward", (PyCFunction)(void (*)(void))forward, METH_FASTCALL, NULL},
+    {"backward", (PyCFunction)(void (*)(void))backward, METH_FASTCALL, NULL},
+    {"step", (PyCFunction)(void (*)(void))step, METH_FASTCALL, NULL},
+    {NULL, NULL, 0, NULL},
+};
+static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", NULL, -1, methods, NULL, NULL, NULL, NULL};
+
+PyMODINIT_FUNC PyInit__marshal(void) {
+    s_dtype = PyUnicode_InternFromString("dtype");
+    s_shape = PyUnicode_InternFromString("shape");
+    s_stride = PyUnicode_InternFromString("stride");
+    s_data_ptr = PyUnicode_InternFromString("data_ptr");
+    s_get_device = PyUnicode_InternFromString("get_device");
+    s_device = PyUnicode_InternFromString("device");
+    s_empty_kw = Py_BuildValue("(ss)", "dtype", "device");
+    if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_get_device || !s_device || !s_empty_kw) return NULL;
+    return PyModule_Create(&module);
+}

@@ -12,8 +12,13 @@ stream.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 
-from . import _check, _ptr, _stream, load_library
+from . import HERE, _check, _ptr, _stream, load_library
+
+# plain calls of the recurrence are marshalled in C where that was built
+_MARSHAL = os.path.join(HERE, "_build", "_marshal.so")
 
 ELEMS = {"f32": 0, "f16": 1, "bf16": 2}
 FORMS = {"decay": 0, "log": 1, "sigmoid": 2}
@@ -111,20 +116,25 @@ def trsm_orthogonalize_workspace_bytes(in_dtype, m, n, batch, steps=5) -> int:
 
 
 # ------------------------------------------------------------------ torch tensors
-_torch = _f32 = _empty = _current_device = _current_stream = None
+_torch = _f32 = _empty = _current_device = _current_stream = _marshal = None
 _elem = {}
 
 
 def _load_torch():
     """torch, with what the calls below use of it at hand: a call's own work on
     the host is a good part of a small one's time."""
-    global _torch, _f32, _empty, _current_device, _current_stream
+    global _torch, _f32, _empty, _current_device, _current_stream, _marshal
     if _torch is None:
         import torch
         _elem.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
         _f32, _empty = torch.float32, torch.empty
         _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         _library()
+        if os.path.exists(_MARSHAL):
+            spec = importlib.util.spec_from_file_location("_marshal", _MARSHAL)
+            _marshal = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(_marshal)
+            _marshal.setup(torch, tuple(FORMS))
         _torch = torch
     return _torch
 
@@ -194,6 +204,10 @@ def _gate(gate, offsets):
 def _forward(gate, x, h0, form, offsets):
     if _torch is None:
         _load_torch()
+    if _marshal is not None:
+        r = _marshal.forward(gate, x, h0, form, offsets)
+        if r is not None:
+            return r if type(r) is tuple else _check("trsm_linrec_forward", r)
     code, batch, T, D, dev, po = _gate(gate, offsets)
     kind = FORMS[form] if form in FORMS else _code(FORMS, form, "form")
     shape, dtype, device = gate.shape, gate.dtype, gate.device
@@ -213,6 +227,10 @@ def linear_recurrence_backward(gate, x, h, dh, h0=None, dh_last=None, *, form="d
     (dh_last None: zero).  ``x`` may be None unless form is "sigmoid"."""
     if _torch is None:
         _load_torch()
+    if _marshal is not None:
+        r = _marshal.backward(gate, x, h, dh, h0, dh_last, form, offsets)
+        if r is not None:
+            return r if type(r) is tuple else _check("trsm_linrec_backward", r)
     code, batch, T, D, dev, po = _gate(gate, offsets)
     kind = FORMS[form] if form in FORMS else _code(FORMS, form, "form")
     shape, dtype, device = gate.shape, gate.dtype, gate.device
@@ -306,6 +324,10 @@ def linear_recurrence_step(gate, x, state, *, form="decay", slots=None, out_stat
     as (batch, D) of gate's type."""
     if _torch is None:
         _load_torch()
+    if _marshal is not None:
+        r = _marshal.step(gate, x, state, form, slots, out_state)
+        if r is not None:
+            return _check("trsm_linrec_step", r) if type(r) is int else r
     shape, dtype, dev = gate.shape, gate.dtype, gate.get_device()
     code = _elem.get(dtype)
     if dev < 0:
