@@ -166,10 +166,14 @@ __device__ __forceinline__ float min_nan(float x, float y) {  // NaN if either i
     return r;
 }
 
-// a and 1 - a of a gate value.  Gates of 16 bits take the hardware's
-// exponential, which is far closer than the gate's own rounding.  The
-// reciprocal is refined: an error of one sign in every token's decay adds up
-// over a long memory (7e-6 of dh0 over 4096 tokens with the bare one).
+// a and 1 - a of a gate value.  An error of one sign in every token's decay
+// adds up over a long memory (2e-5 of the last state over 65536 tokens for one
+// of 2e-8), so the logarithm's exponential is the library's, which what the
+// gates were trained with will have used as well (193 us for 1 x 65536 x 2048
+// bf16; 167 with the hardware's), and the sigmoid's reciprocal is refined (7e-6
+// of dh0 over 4096 tokens with the bare one).  The sigmoid's exponential may be
+// the hardware's for gates of 16 bits: where a is near one it is small beside
+// the one that it is added to.
 //
 // sigmoid: e = exp(-g) held below 2^126, so that neither 1 + e nor e a
 // overflows; a is then 2^-126 where it would be smaller still.
@@ -180,8 +184,7 @@ __device__ __forceinline__ void open_gate(V g, V &a, V &rest) {
     if constexpr (FORM == TRSM_GATE_DECAY) {
         a = g;
     } else if constexpr (FORM == TRSM_GATE_LOG) {
-        if constexpr (kFull) a = each(g, [](float x) { return expf(x); });
-        else a = each(mul_(g, splat<V>(kLog2e)), [](float x) { return exp2_fast(x); });
+        a = each(g, [](float x) { return expf(x); });
     } else {
         V e;
         if constexpr (kFull) e = each(g, [](float x) { return min_nan(expf(-x), 0x1p126f); });
@@ -271,10 +274,11 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
     constexpr int kChannels = L::kChannels, kStretch = L::kStretch;
     constexpr int kSlots = L::kSlots, kParts = L::kParts, kPartSlots = L::kPartSlots;
     constexpr bool kSigmoid = FORM == TRSM_GATE_SIGMOID;
-    // The forward sigmoid keeps a and u of its tokens between the two walks
-    // where they are few (their exponential and reciprocal cost more than the
-    // registers); otherwise the gate is opened again.
-    constexpr bool kKeep = kSigmoid && !BWD && ROWS * VEC <= 32;
+    // The forward pass keeps a and u of its tokens between the two walks: 64
+    // registers cost less than opening the gates again (16% of the time of 1 x
+    // 65536 x 2048 bf16 log).  The backward pass has none to spare, and neither
+    // has the shifting form but for the sigmoid.
+    constexpr bool kKeep = !BWD && ROWS * VEC <= 32 && (kSigmoid || !L::SHIFT);
     using P = Pack<T, VEC>;
     using V = typename Lane<VEC>::V;
     constexpr int kN = Lane<VEC>::kCount;
@@ -812,17 +816,21 @@ int run_layout(const LinrecArgs &a, cudaStream_t st) {
     // Rows off the 16-byte boundaries: 256 threads (1 x 65536 x 2047 bf16 505
     // us, 4 x 2048 x 2047 76 us; 128 threads 593 and 64).
     if (!vec) return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 8, 256, kRows, BWD ? 1 : 2, true, true, 2>>(a, st);
-    // Otherwise 128 threads, and as many channels a CTA as leave the GPU full
-    // with clusters of eight: 4 x 2048 x 2048 29 us with 8 lanes, 46 with 4; 1 x
-    // 65536 x 2048 198 us with 4 lanes, 232 with 8; 1 x 65536 x 512 85 us with 2
-    // lanes, 129 with 4.  Packed sequences are few long ones as far as the host
-    // knows.
-    auto units = [&](int lanes) { return a.batch * ((a.D + lanes * kVec - 1) / (lanes * kVec)); };
+    // Otherwise by the units of 8 lanes, a sequence's channels each, that there
+    // are (bf16, us, with 128 threads of 8, 4, 2 lanes and 256 threads of 8):
+    // many, 128 x 8 (4 x 2048 x 2048: 27, 46, -, 37); some, 256 x 8, and in the
+    // backward pass 128 x 4 (1 x 65536 x 2048: 217, 174, 235, 167; backward 1 x
+    // 16384 x 2048: 114, 78, 105, 83); few, 128 x 2 (1 x 65536 x 512: 175, 113,
+    // 80, 117).  Packed sequences are few long ones as far as the host knows.
+    const int64_t units = a.batch * ((a.D + 8 * kVec - 1) / (8 * kVec));
     if constexpr (!PACKED) {
-        if (units(8) >= 64) return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 8, 128, kRows, 2, false, false, 4>>(a, st);
-        if (units(4) < 64) return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 2, 128, kRows, 2, false, false, 4>>(a, st);
+        if (units >= 64) return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 8, 128, kRows, 2, false, false, 4>>(a, st);
+        if (units < 24) return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 2, 128, kRows, 2, false, false, 4>>(a, st);
+        if constexpr (!BWD)
+            return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 8, 256, kRows, 2, false, false, 2>>(a, st);
     }
-    return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 4, 128, kRows, 2, false, false, 4>>(a, st);
+    if constexpr (BWD || PACKED)
+        return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 4, 128, kRows, 2, false, false, 4>>(a, st);
 }
 
 template <typename T, int FORM, bool BWD>
