@@ -73,7 +73,8 @@ def errors(got, want):
 
 SHAPES = [(1, 1, 1), (2, 1, 500), (2, 500, 1), (3, 2, 3), (4, 17, 5), (5, 64, 64), (3, 65, 64), (2, 100, 1001),
           (1, 256, 257), (2, 300, 130), (1, 513, 700), (1, 1000, 384), (40, 32, 48), (3, 128, 128), (2, 129, 128),
-          (2, 31, 1200), (2, 33, 600), (2, 65, 240), (1, 128, 300), (1, 120, 320), (2, 1600, 20)]
+          (2, 31, 1200), (2, 33, 600), (2, 65, 240), (1, 128, 300), (1, 120, 320), (2, 1600, 20),
+          (3, 25, 4023), (1, 9, 65), (2, 2000, 61), (1, 127, 2111), (90, 60, 900), (1, 128, 5000), (80, 100, 700)]
 
 
 @pytest.mark.parametrize("name", ["f32", "f16", "bf16"])

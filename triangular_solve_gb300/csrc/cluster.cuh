@@ -25,6 +25,21 @@ __device__ __forceinline__ uint32_t map(uint32_t addr, uint32_t r) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(o) : "r"(addr), "r"(r));
     return o;
 }
+// Plain accesses to another CTA's shared memory, ordered by sync().
+__device__ __forceinline__ float4 load_f32x4(uint32_t cluster_addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_b32x2(uint32_t cluster_addr, uint32_t x, uint32_t y) {
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};\n" ::"r"(cluster_addr), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void store_f64(uint32_t cluster_addr, double x) {
+    asm volatile("st.shared::cluster.f64 [%0], %1;\n" ::"r"(cluster_addr), "d"(x) : "memory");
+}
 // Store into another CTA's shared memory that counts its 8 bytes on that
 // CTA's barrier, which orders it before the waits there.
 __device__ __forceinline__ void send_f32x2(uint32_t cluster_addr, float x, float y, uint32_t cluster_bar) {

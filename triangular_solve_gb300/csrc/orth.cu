@@ -603,21 +603,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                         for (int j = 0; j < 32; ++j)
                             if (j == at) o[j] += diag;
                     }
-                    if (plain) {
-                        const int64_t zo = z * g.strideO;
-                        auto put = [&](int64_t at, float x) {
-                            if (g.bf16) static_cast<__nv_bfloat16 *>(g.O)[at] = __float2bfloat16_rn(x);
-                            else static_cast<__half *>(g.O)[at] = __float2half_rn(x);
-                        };
-                        if (row < g.r) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const int64_t c = col + 32 * half + j;
-                                if (c < N) put(zo + (turned ? c * g.ldo + row : row * g.ldo + c), o[j]);
-                            }
-                        }
-                        continue;
-                    }
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) w[j] = pack_out(o[2 * j], o[2 * j + 1], out_bf16);
@@ -642,7 +627,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                         }
                     }
                 }
-                if (plain) continue;
+                if (plain) {
+                    // rows off the 16-byte boundaries: element by element, but
+                    // whole stretches of a row of O at a time
+                    __syncwarp();
+                    uint16_t *const O = static_cast<uint16_t *>(g.O) + z * g.strideO;
+                    if (turned) {
+                        const uint16_t *b = reinterpret_cast<const uint16_t *>(out) + lane;
+                        for (int j = 0; j < 64 && col + j < N; ++j)
+                            if (row < g.r) O[(int64_t)(col + j) * g.ldo + row] = b[j * 32];
+                    } else {
+                        for (int i = 0; i < 32 && row0 + i < g.r; ++i) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int c = lane + 32 * h;
+                                if (col + c < N)
+                                    O[(int64_t)(row0 + i) * g.ldo + col + c] = *reinterpret_cast<const uint16_t *>(
+                                        out + i * 128 + ((c / 8) ^ (i & 7)) * 16 + c % 8 * 2);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    continue;
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -946,7 +953,7 @@ int run(const OrthArgs &a, unsigned long long tails, cudaStream_t st) {
 }  // namespace orth
 
 size_t orth_workspace_bytes(int, int64_t m, int64_t n, int64_t batch, int64_t steps) {
-    if (orth_small_usable(m, n, steps)) return 0;
+    if (orth_small_usable(m, n, batch, steps)) return 0;
     return orth::Layout(m, n, batch).total();
 }
 
@@ -954,7 +961,7 @@ int orth_run(const OrthArgs &a, cudaStream_t st) {
     unsigned long long tails = 0;
     for (int k = 0; k < a.steps; ++k)
         if (orth::has_tail(a.coef, a.steps, k, a.in_dtype != TRSM_ELEM_F32)) tails |= 1ull << k;
-    if (orth_small_usable(a.m, a.n, a.steps)) return orth_small(a, tails, st);
+    if (orth_small_usable(a.m, a.n, a.batch, a.steps)) return orth_small(a, tails, st);
     return orth::run(a, tails, st);
 }
 

@@ -22,9 +22,9 @@ struct OrthArgs {
 };
 size_t orth_workspace_bytes(int in_dtype, int64_t m, int64_t n, int64_t batch, int64_t steps);
 int orth_run(const OrthArgs &a, cudaStream_t st);
-// Small matrices, whole in one CTA each (orth_small.cu), without a workspace;
+// Matrices of few rows, each whole in one CTA or cluster (orth_small.cu), without a workspace;
 // tails: bit k says that X_k is held as head and tail.
-bool orth_small_usable(int64_t m, int64_t n, int64_t steps);
+bool orth_small_usable(int64_t m, int64_t n, int64_t batch, int64_t steps);
 int orth_small(const OrthArgs &a, unsigned long long tails, cudaStream_t st);
 
 }  // namespace trsm

@@ -1,20 +1,25 @@
-// Newton-Schulz orthogonalisation of small matrices: one CTA takes one matrix
-// from the norm to the result, with X (head and tail), S and C in shared
-// memory throughout.
+// Newton-Schulz orthogonalisation of matrices with few rows: one CTA, or a
+// cluster of up to eight, takes one matrix from the norm to the result, with X
+// (head and tail), S and C in shared memory throughout.
 //
-// A matrix of at most 128 rows (after transposition) is far too small for a
+// A matrix of at most 128 rows (after transposition) is far too low for a
 // 256-row tensor-core tile, and its fifteen dependent products are bound by
 // the way from one to the next, not by their arithmetic.  So the products
 // are warp-level matrix instructions (m16n8k16, f16 factors, f32 sums) whose
 // operands come straight from shared memory: a product costs a barrier
 // instead of a launch and two trips through L2.
+//
+// In a cluster each CTA has a part of the columns.  Its part of S = X X^T goes
+// to the others through distributed shared memory, each CTA summing a share of
+// the entries in the order of the ranks; C is computed by all of them, and C X
+// again by each for its columns.
 #include <math.h>
 #include <stdint.h>
 
 #include <cuda_runtime.h>
 
+#include "cluster.cuh"
 #include "common.cuh"
-#include "mbarrier.cuh"
 #include "orth.h"
 #include "orth_convert.cuh"
 #include "trsm_model.h"
@@ -22,9 +27,11 @@
 namespace trsm {
 namespace orth {
 
+constexpr int kMostCtas = 8;
+
 struct SmallArgs {
     Input in;
-    int r, c, cp, ldx;  // c rounded up to 16; row length of X in shared memory
+    int r, c, cp, ldx;  // columns of a CTA, a multiple of 16; row length of X in shared memory
     int tall, steps, any_tail;
     unsigned long long tails;  // bit k: X_k has a tail
     double eps;
@@ -91,8 +98,9 @@ __device__ __forceinline__ void tile_product(float (&acc)[WM / 16][WN / 8][4], u
     }
 }
 
-template <typename T, int R, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, SmallShape<R, WARPS>::kBlocks)
+// CLUSTER: a cluster a matrix (apart, for the registers of its sums).
+template <typename T, int R, int WARPS, bool CLUSTER>
+__global__ void __launch_bounds__(32 * WARPS, CLUSTER && R == 128 ? 1 : SmallShape<R, WARPS>::kBlocks)
     small_kernel(const __grid_constant__ SmallArgs g) {
     using W = SmallShape<R, WARPS>;
     constexpr int WM = W::WM, WN = W::WN, kWarps = WARPS, kThreads = 32 * WARPS;
@@ -103,10 +111,20 @@ __global__ void __launch_bounds__(32 * WARPS, SmallShape<R, WARPS>::kBlocks)
     float *const scratch = reinterpret_cast<float *>(C + R * W::ld);
     __shared__ Scale scale;
 
+    __shared__ double sums[kMostCtas];
+
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t z = blockIdx.x;
+    const int ctas = CLUSTER ? (int)cluster::size() : 1, rank = CLUSTER ? (int)cluster::rank() : 0;
+    const int64_t z = blockIdx.x / ctas;
+    const int c0 = rank * g.cp, cols = max(0, min(g.cp, g.c - c0));  // this CTA's columns of X
     const T *G = static_cast<const T *>(g.in.G) + z * g.in.stride;
-    const int m = (int)g.in.m, n = (int)g.in.n, per = (n + 7) / 8;
+    // its groups of 8 along G's rows: X's columns, or for a tall G its rows
+    const int n = (int)g.in.n, per = ((g.tall ? n : cols) + 7) / 8, groups = (g.tall ? cols : g.r) * per;
+    auto load = [&](int e, float (&v)[8]) {
+        const int i = e / per, j = e % per * 8;
+        if (g.tall) load_8<T>(G + (int64_t)(c0 + i) * g.in.ld, j, n, g.in.vec, v);
+        else load_8<T>(G + (int64_t)i * g.in.ld, c0 + j, min(n, c0 + cols), g.in.vec, v);
+    };
 
     // |G|_F, while X is set to zero (its padding stays so).  The first kHeld
     // groups of a thread stay in registers for X_0, the rest is read again.
@@ -114,21 +132,27 @@ __global__ void __launch_bounds__(32 * WARPS, SmallShape<R, WARPS>::kBlocks)
     float held[kHeld][8];
     Squares sq;
 #pragma unroll
-    for (int q = 0; q < kHeld; ++q) {
-        const int e = tid + q * kThreads;
-        if (e < m * per) load_8<T>(G + (int64_t)(e / per) * g.in.ld, e % per * 8, n, g.in.vec, held[q]);
-    }
+    for (int q = 0; q < kHeld; ++q)
+        if (tid + q * kThreads < groups) load(tid + q * kThreads, held[q]);
     for (int e = tid; e < R * g.ldx * (g.any_tail ? 2 : 1) / 8; e += kThreads)
         reinterpret_cast<uint4 *>(Xh)[e] = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int q = 0; q < kHeld; ++q)
-        if (tid + q * kThreads < m * per) sq.add_8(held[q]);
-    for (int e = tid + kHeld * kThreads; e < m * per; e += kThreads) {
+        if (tid + q * kThreads < groups) sq.add_8(held[q]);
+    for (int e = tid + kHeld * kThreads; e < groups; e += kThreads) {
         float v[8];
-        load_8<T>(G + (int64_t)(e / per) * g.in.ld, e % per * 8, n, g.in.vec, v);
+        load(e, v);
         sq.add_8(v);
     }
-    const double sum = block_sum(sq);
+    double sum = block_sum(sq);
+    if constexpr (CLUSTER) {
+        cluster::sync();  // every CTA has started
+        if (tid == 0)
+            for (int k = 0; k < ctas; ++k) cluster::store_f64(cluster::map(smem_u32(&sums[rank]), k), sum);
+        cluster::sync();
+        sum = 0;
+        for (int k = 0; k < ctas; ++k) sum += sums[k];
+    }
     if (tid == 0) scale = scale_from(sum, g.eps);
     __syncthreads();
     const float rho = scale.rho;
@@ -154,10 +178,10 @@ __global__ void __launch_bounds__(32 * WARPS, SmallShape<R, WARPS>::kBlocks)
     };
 #pragma unroll
     for (int q = 0; q < kHeld; ++q)
-        if (tid + q * kThreads < m * per) put(tid + q * kThreads, held[q]);
-    for (int e = tid + kHeld * kThreads; e < m * per; e += kThreads) {
+        if (tid + q * kThreads < groups) put(tid + q * kThreads, held[q]);
+    for (int e = tid + kHeld * kThreads; e < groups; e += kThreads) {
         float v[8];
-        load_8<T>(G + (int64_t)(e / per) * g.in.ld, e % per * 8, n, g.in.vec, v);
+        load(e, v);
         put(e, v);
     }
     __syncthreads();
@@ -174,15 +198,26 @@ __global__ void __launch_bounds__(32 * WARPS, SmallShape<R, WARPS>::kBlocks)
             const int k0 = cut * each, k1 = k0 + each < all ? k0 + each : all;
             if (k0 < k1) tile_product<WM, WN>(acc, xh, g.ldx, m0, xh, g.ldx, n0, 16 * k0, k1 - k0);
             const float alpha = kScaleS / (kScaleX * kScaleX) * (s == 0 ? rho * rho : 1.f);
-            if constexpr (W::kCut == 1) {
+            // the sums of a tile to S, or to this CTA's part of it
+            float *const part = reinterpret_cast<float *>(S);  // over S and C, which are free here
+            auto store = [&]() {
 #pragma unroll
                 for (int i = 0; i < WM / 16; ++i)
 #pragma unroll
                     for (int j = 0; j < WN / 8; ++j)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            *reinterpret_cast<__half2 *>(S + (m0 + 16 * i + row + 8 * h) * W::ld + n0 + 8 * j + col) =
-                                __floats2half2_rn(alpha * acc[i][j][2 * h], alpha * acc[i][j][2 * h + 1]);
+                        for (int h = 0; h < 2; ++h) {
+                            const int y = m0 + 16 * i + row + 8 * h, x = n0 + 8 * j + col;
+                            if constexpr (!CLUSTER)
+                                *reinterpret_cast<__half2 *>(S + y * W::ld + x) =
+                                    __floats2half2_rn(alpha * acc[i][j][2 * h], alpha * acc[i][j][2 * h + 1]);
+                            else
+                                *reinterpret_cast<float2 *>(part + y * R + x) =
+                                    make_float2(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
+                        }
+            };
+            if constexpr (W::kCut == 1) {
+                store();
             } else {
                 float *mine = scratch + warp * (WM * WN);
 #pragma unroll
@@ -197,18 +232,46 @@ __global__ void __launch_bounds__(32 * WARPS, SmallShape<R, WARPS>::kBlocks)
 #pragma unroll
                     for (int i = 0; i < WM / 16; ++i)
 #pragma unroll
-                        for (int j = 0; j < WN / 8; ++j) {
+                        for (int j = 0; j < WN / 8; ++j)
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
                                 for (int p = 1; p < W::kCut; ++p)
                                     acc[i][j][q] += scratch[(p * W::kTiles + tile) * (WM * WN) +
                                                             ((i * (WN / 8) + j) * 4 + q) * 32 + lane];
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                *reinterpret_cast<__half2 *>(S + (m0 + 16 * i + row + 8 * h) * W::ld + n0 + 8 * j + col) =
-                                    __floats2half2_rn(alpha * acc[i][j][2 * h], alpha * acc[i][j][2 * h + 1]);
-                        }
+                    store();
                 }
+            }
+            if constexpr (CLUSTER) {
+                // a share of the entries, four at a time, summed over the CTAs
+                constexpr int kMost = (R * R / 4 / 2 + kThreads - 1) / kThreads;
+                float4 total[kMost];
+                const int share = R * R / 4 / ctas;
+                cluster::sync();
+#pragma unroll
+                for (int q = 0; q < kMost; ++q) {
+                    const int e = tid + q * kThreads;
+                    if (e >= share) break;
+                    const uint32_t at = smem_u32(part + 4 * (rank * share + e));
+                    total[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k = 0; k < ctas; ++k) {
+                        const float4 v = cluster::load_f32x4(cluster::map(at, k));
+                        total[q] = make_float4(total[q].x + v.x, total[q].y + v.y, total[q].z + v.z, total[q].w + v.w);
+                    }
+                }
+                cluster::sync();  // all parts have been read
+#pragma unroll
+                for (int q = 0; q < kMost; ++q) {
+                    const int e = tid + q * kThreads;
+                    if (e >= share) break;
+                    const int at = 4 * (rank * share + e);
+                    const uint32_t to = smem_u32(S + at / R * W::ld + at % R);
+                    const __half2 lo = __floats2half2_rn(alpha * total[q].x, alpha * total[q].y);
+                    const __half2 hi = __floats2half2_rn(alpha * total[q].z, alpha * total[q].w);
+                    for (int k = 0; k < ctas; ++k)
+                        cluster::store_b32x2(cluster::map(to, k), *reinterpret_cast<const uint32_t *>(&lo),
+                                             *reinterpret_cast<const uint32_t *>(&hi));
+                }
+                cluster::sync();
             }
         }
         __syncthreads();
@@ -299,18 +362,21 @@ __global__ void __launch_bounds__(32 * WARPS, SmallShape<R, WARPS>::kBlocks)
     uint16_t *O = static_cast<uint16_t *>(g.O) + z * g.strideO;
     const uint16_t *X = reinterpret_cast<const uint16_t *>(Xh);
     if (!g.tall && g.vec) {
-        for (int e = tid; e < m * per; e += kThreads) {
+        for (int e = tid; e < groups; e += kThreads) {
             const int i = e / per, j = e % per * 8;
-            if (j + 8 <= n) {
-                *reinterpret_cast<uint4 *>(O + i * g.ldo + j) = *reinterpret_cast<const uint4 *>(X + i * g.ldx + j);
+            uint16_t *to = O + i * g.ldo + c0 + j;
+            if (j + 8 <= cols) {
+                *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(X + i * g.ldx + j);
             } else {
-                for (int k = j; k < n; ++k) O[i * g.ldo + k] = X[i * g.ldx + k];
+                for (int k = j; k < cols; ++k) to[k - j] = X[i * g.ldx + k];
             }
         }
     } else {
-        for (int e = tid; e < m * n; e += kThreads) {
-            const int i = e / n, j = e % n;
-            O[i * g.ldo + j] = g.tall ? X[j * g.ldx + i] : X[i * g.ldx + j];
+        const int width = g.tall ? n : cols, all = (g.tall ? cols : g.r) * width;
+        for (int e = tid; e < all; e += kThreads) {
+            const int i = e / width, j = e % width;
+            if (g.tall) O[(c0 + i) * g.ldo + j] = X[j * g.ldx + i];
+            else O[i * g.ldo + c0 + j] = X[i * g.ldx + j];
         }
     }
 }
@@ -318,43 +384,64 @@ __global__ void __launch_bounds__(32 * WARPS, SmallShape<R, WARPS>::kBlocks)
 // ------------------------------------------------------------------ launch
 constexpr size_t kMostSmem = 224 * 1024;
 
+int columns_of(int64_t c, int ctas) { return (int)((c + 16 * ctas - 1) / (16 * ctas)) * 16; }
+// CTAs that a matrix of c columns needs, or 0 where eight do not suffice.
 // With a tail, which the coefficients may ask for or not: whether a call
 // needs a workspace depends on the shape alone.
-template <int R> bool fits(int64_t c) {
-    return SmallShape<R, 8>::smem((int)((c + 15) / 16 * 16 + 8), true) <= kMostSmem;
-}
-// Rows of the kernel that takes r x c matrices, or 0.
-int small_rows(int64_t r, int64_t c) {
-    if (c > 4096) return 0;
-    if (r <= 32) return fits<32>(c) ? 32 : 0;
-    if (r <= 64) return fits<64>(c) ? 64 : 0;
-    if (r <= 128) return fits<128>(c) ? 128 : 0;
+template <int R> int least_ctas(int64_t c) {
+    for (int k = 1; k <= kMostCtas; k *= 2)
+        if (SmallShape<R, 8>::smem(columns_of(c, k) + 8, true) <= kMostSmem) return k;
     return 0;
 }
+int small_rows(int64_t r) { return r <= 32 ? 32 : r <= 64 ? 64 : 128; }
+int small_ctas(int64_t r, int64_t c) {
+    if (r > 128) return 0;
+    const int rows = small_rows(r);
+    return rows == 32 ? least_ctas<32>(c) : rows == 64 ? least_ctas<64>(c) : least_ctas<128>(c);
+}
 
-template <typename T, int R, int WARPS> int launch(const SmallArgs &g, int64_t batch, cudaStream_t st) {
+template <typename T, int R, int WARPS, bool CLUSTER> int launch(const SmallArgs &g, int64_t batch, int ctas, cudaStream_t st) {
     const size_t smem = SmallShape<R, WARPS>::smem(g.ldx, g.any_tail);
-    const cudaError_t e = cudaFuncSetAttribute(small_kernel<T, R, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(small_kernel<T, R, WARPS, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)kMostSmem);
     if (e != cudaSuccess) return cuda_status(e);
-    small_kernel<T, R, WARPS><<<(unsigned)batch, 32 * WARPS, smem, st>>>(g);
-    return launch_status();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(batch * ctas));
+    cfg.blockDim = dim3(32 * WARPS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)ctas;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, small_kernel<T, R, WARPS, CLUSTER>, g));
 }
-template <typename T> int launch_rows(const SmallArgs &g, int rows, int64_t batch, cudaStream_t st) {
-    if (rows == 128) return launch<T, 128, 8>(g, batch, st);
+template <typename T> int launch_rows(const SmallArgs &g, int rows, int64_t batch, int ctas, cudaStream_t st) {
+    if (ctas > 1)
+        return rows == 32   ? launch<T, 32, 8, true>(g, batch, ctas, st)
+               : rows == 64 ? launch<T, 64, 8, true>(g, batch, ctas, st)
+                            : launch<T, 128, 8, true>(g, batch, ctas, st);
+    if (rows == 128) return launch<T, 128, 8, false>(g, batch, 1, st);
     // four warps keep more of the smallest matrices on an SM (512 of 32 x 32: 15
     // us, with eight 24; 1024 of 64 x 64: 49, 53), eight finish larger ones
     // sooner (300 of 64 x 128: 28, with four 32; 1 of 64 x 800: 76, 105)
     const bool four = rows * g.c <= 4096;
-    if (rows == 64) return four ? launch<T, 64, 4>(g, batch, st) : launch<T, 64, 8>(g, batch, st);
-    return four ? launch<T, 32, 4>(g, batch, st) : launch<T, 32, 8>(g, batch, st);
+    if (rows == 64) return four ? launch<T, 64, 4, false>(g, batch, 1, st) : launch<T, 64, 8, false>(g, batch, 1, st);
+    return four ? launch<T, 32, 4, false>(g, batch, 1, st) : launch<T, 32, 8, false>(g, batch, 1, st);
 }
 
 }  // namespace orth
 
-bool orth_small_usable(int64_t m, int64_t n, int64_t steps) {
+bool orth_small_usable(int64_t m, int64_t n, int64_t batch, int64_t steps) {
     const int64_t r = m < n ? m : n, c = m < n ? n : m;
-    return steps > 0 && steps < orth::kMaxSteps && orth::small_rows(r, c) > 0;
+    if (steps < 1 || steps >= orth::kMaxSteps) return false;
+    const int ctas = orth::small_ctas(r, c);
+    // Of more than 64 rows, many wide matrices are better off on the large
+    // tiles, which they half fill (113 of 128 x 896: about 230 us against 343 in
+    // clusters of four; 2 of 91 x 1123 81 us in clusters).
+    return ctas == 1 || (ctas > 1 && (r <= 64 || batch * ctas <= 152));
 }
 
 int orth_small(const OrthArgs &a, unsigned long long tails, cudaStream_t st) {
@@ -363,7 +450,10 @@ int orth_small(const OrthArgs &a, unsigned long long tails, cudaStream_t st) {
     g.in = {a.G, a.m, a.n, a.ldg, a.strideG, orth::rows_on_16_bytes(a.G, a.m, a.ldg, a.batch, a.strideG, es)};
     g.r = (int)(a.m < a.n ? a.m : a.n);
     g.c = (int)(a.m < a.n ? a.n : a.m);
-    g.cp = (g.c + 15) / 16 * 16;
+    // as many CTAs a matrix as it needs, and more where there are few matrices
+    int ctas = orth::small_ctas(g.r, g.c);
+    while (ctas < orth::kMostCtas && a.batch * ctas * 2 <= 152 && orth::columns_of(g.c, ctas) > 64) ctas *= 2;
+    g.cp = orth::columns_of(g.c, ctas);
     g.ldx = g.cp + 8;
     g.tall = a.m > a.n;
     g.steps = a.steps;
@@ -376,11 +466,11 @@ int orth_small(const OrthArgs &a, unsigned long long tails, cudaStream_t st) {
     g.bf16 = a.out_dtype == TRSM_ELEM_BF16;
     g.vec = orth::rows_on_16_bytes(a.O, a.m, a.ldo, a.batch, a.strideO, 2);
     for (int i = 0; i < 3 * a.steps; ++i) g.coef[i] = (float)a.coef[i];
-    const int rows = orth::small_rows(g.r, g.c);
+    const int rows = orth::small_rows(g.r);
     switch (a.in_dtype) {
-        case TRSM_ELEM_F32: return orth::launch_rows<float>(g, rows, a.batch, st);
-        case TRSM_ELEM_F16: return orth::launch_rows<__half>(g, rows, a.batch, st);
-        default: return orth::launch_rows<__nv_bfloat16>(g, rows, a.batch, st);
+        case TRSM_ELEM_F32: return orth::launch_rows<float>(g, rows, a.batch, ctas, st);
+        case TRSM_ELEM_F16: return orth::launch_rows<__half>(g, rows, a.batch, ctas, st);
+        default: return orth::launch_rows<__nv_bfloat16>(g, rows, a.batch, ctas, st);
     }
 }
 
