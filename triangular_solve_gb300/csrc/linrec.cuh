@@ -813,16 +813,22 @@ int run_layout(const LinrecArgs &a, cudaStream_t st) {
     bool vec = a.D % kVec == 0 && rows_vec(a, a.gate, sizeof(T)) && rows_vec(a, a.h, sizeof(T));
     if (!BWD || FORM == TRSM_GATE_SIGMOID) vec = vec && rows_vec(a, a.x, sizeof(T));
     if (BWD) vec = vec && rows_vec(a, a.dh, sizeof(T)) && rows_vec(a, a.dgate, sizeof(T)) && rows_vec(a, a.dx, sizeof(T));
+    const int64_t groups = (a.D + 8 * kVec - 1) / (8 * kVec), units = a.batch * groups;
     // Rows off the 16-byte boundaries: 256 threads (1 x 65536 x 2047 bf16 505
-    // us, 4 x 2048 x 2047 76 us; 128 threads 593 and 64).
-    if (!vec) return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 8, 256, kRows, BWD ? 1 : 2, true, true, 2>>(a, st);
+    // us, 4 x 2048 x 2047 76 us; 128 threads 593 and 64), of 2 lanes where there
+    // are few channels.
+    if (!vec) {
+        constexpr int kStages = BWD ? 1 : 2;
+        if (PACKED ? groups == 1 : units < 24)
+            return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 2, 256, kRows, kStages, true, true, 2>>(a, st);
+        return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 8, 256, kRows, kStages, true, true, 2>>(a, st);
+    }
     // Otherwise by the units of 8 lanes, a sequence's channels each, that there
     // are (bf16, us, with 128 threads of 8, 4, 2 lanes and 256 threads of 8):
     // many, 128 x 8 (4 x 2048 x 2048: 27, 46, -, 37); some, 256 x 8, and in the
     // backward pass 128 x 4 (1 x 65536 x 2048: 217, 174, 235, 167; backward 1 x
     // 16384 x 2048: 114, 78, 105, 83); few, 128 x 2 (1 x 65536 x 512: 175, 113,
     // 80, 117).  Packed sequences are few long ones as far as the host knows.
-    const int64_t units = a.batch * ((a.D + 8 * kVec - 1) / (8 * kVec));
     if constexpr (!PACKED) {
         if (units >= 64) return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 8, 128, kRows, 2, false, false, 4>>(a, st);
         if (units < 24) return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 2, 128, kRows, 2, false, false, 4>>(a, st);
