@@ -182,6 +182,33 @@ def test_packed_sequences(env, name, form, lengths, D):
     c.check_backward(h, *grads)
 
 
+# Each number of lanes and threads that the number of channels selects, over
+# more than one step of a cluster.
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 2500, 57), (1, 2500, 327), (1, 2500, 1025), (1, 2500, 640), (2, 1100, 1024),
+                                   (7, 600, 648)], ids=str)
+def test_plans_of_batched_sequences(env, name, shape):
+    torch, tg = env
+    b, T, D = shape
+    c = Case(torch, name, "sigmoid", [T] * b, D, state=True, seed=T + D)
+    g, x, dh = (t.view(b, T, D) for t in (c.gate, c.x, c.dh))
+    h, last = tg.linear_recurrence(g, x, c.h0, form="sigmoid")
+    c.check_forward(h.view(-1, D), last)
+    grads = tg.linear_recurrence_backward(g, x, h, dh, c.h0, c.dlast, form="sigmoid")
+    c.check_backward(h.view(-1, D), grads[0].view(-1, D), grads[1].view(-1, D), grads[2])
+
+
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [57, 327, 1025, 320, 648])
+def test_plans_of_packed_sequences(env, name, D):
+    torch, tg = env
+    c = Case(torch, name, "log", [3, 0, 2300, 40, 600], D, state=True, seed=D)
+    h, last = tg.linear_recurrence(c.gate, c.x, c.h0, form="log", offsets=c.offsets)
+    c.check_forward(h, last)
+    grads = tg.linear_recurrence_backward(c.gate, c.x, h, c.dh, c.h0, c.dlast, form="log", offsets=c.offsets)
+    c.check_backward(h, *grads)
+
+
 def test_empty_sequences_pass_their_state_on(env):
     torch, tg = env
     h0 = torch.randn(4, 24, device="cuda")

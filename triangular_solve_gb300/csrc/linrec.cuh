@@ -820,30 +820,43 @@ int run_layout(const LinrecArgs &a, cudaStream_t st) {
     bool vec = a.D % kVec == 0 && rows_vec(a, a.gate, sizeof(T)) && rows_vec(a, a.h, sizeof(T));
     if (!BWD || FORM == TRSM_GATE_SIGMOID) vec = vec && rows_vec(a, a.x, sizeof(T));
     if (BWD) vec = vec && rows_vec(a, a.dh, sizeof(T)) && rows_vec(a, a.dgate, sizeof(T)) && rows_vec(a, a.dx, sizeof(T));
-    const int64_t groups = (a.D + 8 * kVec - 1) / (8 * kVec), units = a.batch * groups;
-    // Rows off the 16-byte boundaries: 256 threads (1 x 65536 x 2047 bf16 505
-    // us, 4 x 2048 x 2047 76 us; 128 threads 593 and 64), of 2 lanes where there
-    // are few channels.
+    // The plan goes by the units of 8 lanes that there are: the channels of a
+    // sequence, of packed sequences of one alone (they are few long ones as far
+    // as the host knows).  Fewer lanes make more and longer stretches of few
+    // units; too many for one wave of CTAs, and their narrow rows cost more than
+    // the steps that they save.  Times below are bf16, us.
+    const int64_t groups = (a.D + 8 * kVec - 1) / (8 * kVec), units = PACKED ? groups : a.batch * groups;
     if (!vec) {
+        // Rows off the 16-byte boundaries, 256 threads (128 are slower or no
+        // faster) of 8, 4, 2 lanes: forward 1 x 65536 x 2047 569, 635, 1170;
+        // backward 1 x 28672 x 429 279, 164, 219; forward 1 x 32768 x 221 packed
+        // 217, 121, 86.
         constexpr int kStages = BWD ? 1 : 2;
-        if (PACKED ? groups == 1 : units < 24)
-            return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 2, 256, kRows, kStages, true, true, 2>>(a, st);
-        return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 8, 256, kRows, kStages, true, true, 2>>(a, st);
+        using Wide = Plan<kVec, 8, 256, kRows, kStages, true, true, 2>;
+        const bool one_step = a.T <= kMaxCluster * Wide::kStretch;
+        if (units >= 14 || one_step) return launch_scan<T, FORM, BWD, PACKED, Wide>(a, st);
+        if (units >= 5)
+            return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 4, 256, kRows, kStages, true, true, 2>>(a, st);
+        return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 2, 256, kRows, kStages, true, true, 2>>(a, st);
     }
-    // Otherwise by the units of 8 lanes, a sequence's channels each, that there
-    // are (bf16, us, with 128 threads of 8, 4, 2 lanes and 256 threads of 8):
-    // many, 128 x 8 (4 x 2048 x 2048: 27, 46, -, 37); some, 256 x 8, and in the
-    // backward pass 128 x 4 (1 x 65536 x 2048: 217, 174, 235, 167; backward 1 x
-    // 16384 x 2048: 114, 78, 105, 83); few, 128 x 2 (1 x 65536 x 512: 175, 113,
-    // 80, 117).  Packed sequences are few long ones as far as the host knows.
-    if constexpr (!PACKED) {
-        if (units >= 64) return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 8, 128, kRows, 2, false, false, 4>>(a, st);
-        if (units < 24) return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 2, 128, kRows, 2, false, false, 4>>(a, st);
-        if constexpr (!BWD)
-            return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 8, 256, kRows, 2, false, false, 2>>(a, st);
+    if constexpr (PACKED) {
+        // 256 threads of 8 and of 4 lanes: 4 sequences in 32768 x 1024 49, 60,
+        // backward 105, 119; x 512 47, 35, backward 94, 66.
+        if (groups >= 10) return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 8, 256, kRows, 2, false, false, 2>>(a, st);
+        return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 4, 256, kRows, 2, false, false, 2>>(a, st);
+    } else {
+        // 128 threads of 8, 4, 2 lanes: forward 4 x 2048 x 2048 27, 33, 39; 1 x
+        // 32768 x 2048 124, 102, 125, backward 279, 195, 260; x 1024 119, 72, 68,
+        // backward 228, 150, 137; x 512 104, 68, 47, backward 207, 123, 90.  f32,
+        // whose lanes are half as many channels: 1 x 8192 x 1024 29, 43, 53; x
+        // 512 26, 23, 35; x 256 23, 18, 18.
+        constexpr bool kWide = sizeof(T) == 4;
+        if (units >= (kWide ? 20 : 64))
+            return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 8, 128, kRows, 2, false, false, 4>>(a, st);
+        if (units >= (kWide ? 10 : 20))
+            return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 4, 128, kRows, 2, false, false, 4>>(a, st);
+        return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 2, 128, kRows, 2, false, false, 4>>(a, st);
     }
-    if constexpr (BWD || PACKED)
-        return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 4, 128, kRows, 2, false, false, 4>>(a, st);
 }
 
 template <typename T, int FORM, bool BWD>
@@ -851,15 +864,12 @@ int run(const LinrecArgs &a, cudaStream_t st) {
     return a.offsets ? run_layout<T, FORM, BWD, true>(a, st) : run_layout<T, FORM, BWD, false>(a, st);
 }
 
-template <typename T>
-int run_form(const LinrecArgs &a, int form, bool backward, cudaStream_t st) {
+template <typename T, bool BWD>
+int run_form(const LinrecArgs &a, int form, cudaStream_t st) {
     switch (form) {
-        case TRSM_GATE_DECAY:
-            return backward ? run<T, TRSM_GATE_DECAY, true>(a, st) : run<T, TRSM_GATE_DECAY, false>(a, st);
-        case TRSM_GATE_LOG:
-            return backward ? run<T, TRSM_GATE_LOG, true>(a, st) : run<T, TRSM_GATE_LOG, false>(a, st);
-        default:
-            return backward ? run<T, TRSM_GATE_SIGMOID, true>(a, st) : run<T, TRSM_GATE_SIGMOID, false>(a, st);
+        case TRSM_GATE_DECAY: return run<T, TRSM_GATE_DECAY, BWD>(a, st);
+        case TRSM_GATE_LOG: return run<T, TRSM_GATE_LOG, BWD>(a, st);
+        default: return run<T, TRSM_GATE_SIGMOID, BWD>(a, st);
     }
 }
 

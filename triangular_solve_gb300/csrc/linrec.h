@@ -1,6 +1,6 @@
 // Internal interface of the gated linear recurrence (trsm_linrec_*): the
-// arguments of the kernels and their launchers, one translation unit per
-// element type.
+// arguments of the kernels and their launchers, a translation unit per
+// element type and direction.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -40,9 +40,12 @@ struct LinrecStepArgs {
     int64_t y_stride;
 };
 
-int linrec_run_f32(const LinrecArgs &a, int form, bool backward, cudaStream_t st);
-int linrec_run_f16(const LinrecArgs &a, int form, bool backward, cudaStream_t st);
-int linrec_run_bf16(const LinrecArgs &a, int form, bool backward, cudaStream_t st);
+int linrec_forward_f32(const LinrecArgs &a, int form, cudaStream_t st);
+int linrec_backward_f32(const LinrecArgs &a, int form, cudaStream_t st);
+int linrec_forward_f16(const LinrecArgs &a, int form, cudaStream_t st);
+int linrec_backward_f16(const LinrecArgs &a, int form, cudaStream_t st);
+int linrec_forward_bf16(const LinrecArgs &a, int form, cudaStream_t st);
+int linrec_backward_bf16(const LinrecArgs &a, int form, cudaStream_t st);
 int linrec_step_f32(const LinrecStepArgs &a, int form, cudaStream_t st);
 int linrec_step_f16(const LinrecStepArgs &a, int form, cudaStream_t st);
 int linrec_step_bf16(const LinrecStepArgs &a, int form, cudaStream_t st);

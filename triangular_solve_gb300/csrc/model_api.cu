@@ -38,9 +38,9 @@ bool rows_disjoint(int64_t rows, int64_t D, int64_t st) { return rows <= 1 || ma
 
 int run(int dtype, const LinrecArgs &a, int form, bool backward, cudaStream_t st) {
     switch (dtype) {
-        case TRSM_ELEM_F32: return linrec_run_f32(a, form, backward, st);
-        case TRSM_ELEM_F16: return linrec_run_f16(a, form, backward, st);
-        default: return linrec_run_bf16(a, form, backward, st);
+        case TRSM_ELEM_F32: return backward ? linrec_backward_f32(a, form, st) : linrec_forward_f32(a, form, st);
+        case TRSM_ELEM_F16: return backward ? linrec_backward_f16(a, form, st) : linrec_forward_f16(a, form, st);
+        default: return backward ? linrec_backward_bf16(a, form, st) : linrec_forward_bf16(a, form, st);
     }
 }
 
