@@ -74,9 +74,9 @@ template <int R, int WARPS> struct SmallShape {
     static constexpr int ld = R + 8;  // of S and C: rows 16 bytes apart in the banks
     static constexpr size_t kScratch = kCut > 1 ? (size_t)WARPS * WM * WN * 4 : 0;
     // CTAs an SM should hold
-    static constexpr int kBlocks = R == 128 ? 2 : 24 / WARPS;
-    static size_t smem(int ldx, bool tail) {
-        return (size_t)R * ldx * 2 * (tail ? 2 : 1) + 2 * (size_t)R * ld * 2 + kScratch;
+    static constexpr int kBlocks = R == 128 ? 2 : 28 / WARPS;
+    static size_t smem(int ldx, bool tail, bool cluster) {
+        return (size_t)R * ldx * 2 * (tail ? 2 : 1) + (cluster ? 2 : 1) * (size_t)R * ld * 2 + kScratch;
     }
 };
 
@@ -111,7 +111,9 @@ __global__ void __launch_bounds__(32 * WARPS, CLUSTER && R == 128 ? 1 : SmallSha
     extern __shared__ __align__(16) unsigned char small_smem[];
     __half *const Xh = reinterpret_cast<__half *>(small_smem);
     __half *const Xl = Xh + (size_t)R * g.ldx;
-    __half *const S = Xh + (size_t)R * g.ldx * (g.any_tail ? 2 : 1), *const C = S + R * W::ld;
+    __half *const S = Xh + (size_t)R * g.ldx * (g.any_tail ? 2 : 1);
+    // C takes S's place; in a cluster the float sums need the room of both
+    __half *const C = CLUSTER ? S + R * W::ld : S;
     float *const scratch = reinterpret_cast<float *>(C + R * W::ld);
     __shared__ Scale scale;
 
@@ -279,22 +281,36 @@ __global__ void __launch_bounds__(32 * WARPS, CLUSTER && R == 128 ? 1 : SmallSha
             }
         }
         __syncthreads();
-        if (cut == 0) {  // C = a I + b S + c S^2
-            float acc[WM / 16][WN / 8][4] = {};
-            tile_product<WM, WN>(acc, sS, W::ld, m0, sS, W::ld, n0, 0, R / 16);
-            const float diag = g.coef[3 * s] * kScaleS, beta = g.coef[3 * s + 1], alpha = g.coef[3 * s + 2] / kScaleS;
+        {  // C = a I + b S + c S^2
+            __half2 out[WM / 16][WN / 8][2];
+            if (cut == 0) {
+                float acc[WM / 16][WN / 8][4] = {};
+                tile_product<WM, WN>(acc, sS, W::ld, m0, sS, W::ld, n0, 0, R / 16);
+                const float diag = g.coef[3 * s] * kScaleS, beta = g.coef[3 * s + 1], alpha = g.coef[3 * s + 2] / kScaleS;
 #pragma unroll
-            for (int i = 0; i < WM / 16; ++i)
+                for (int i = 0; i < WM / 16; ++i)
 #pragma unroll
-                for (int j = 0; j < WN / 8; ++j)
+                    for (int j = 0; j < WN / 8; ++j)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int y = m0 + 16 * i + row + 8 * h, x = n0 + 8 * j + col;
-                        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(S + y * W::ld + x));
-                        const float o0 = fmaf(beta, b.x, alpha * acc[i][j][2 * h]) + (x == y ? diag : 0.f);
-                        const float o1 = fmaf(beta, b.y, alpha * acc[i][j][2 * h + 1]) + (x + 1 == y ? diag : 0.f);
-                        *reinterpret_cast<__half2 *>(C + y * W::ld + x) = __floats2half2_rn(o0, o1);
-                    }
+                        for (int h = 0; h < 2; ++h) {
+                            const int y = m0 + 16 * i + row + 8 * h, x = n0 + 8 * j + col;
+                            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(S + y * W::ld + x));
+                            const float o0 = fmaf(beta, b.x, alpha * acc[i][j][2 * h]) + (x == y ? diag : 0.f);
+                            const float o1 = fmaf(beta, b.y, alpha * acc[i][j][2 * h + 1]) + (x + 1 == y ? diag : 0.f);
+                            out[i][j][h] = __floats2half2_rn(o0, o1);
+                        }
+            }
+            if constexpr (!CLUSTER) __syncthreads();  // S has been read
+            if (cut == 0) {
+#pragma unroll
+                for (int i = 0; i < WM / 16; ++i)
+#pragma unroll
+                    for (int j = 0; j < WN / 8; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            *reinterpret_cast<__half2 *>(C + (m0 + 16 * i + row + 8 * h) * W::ld + n0 + 8 * j + col) =
+                                out[i][j][h];
+            }
         }
         __syncthreads();
         // X = C X in place: a warp holds 16 columns of X in registers and
@@ -394,7 +410,7 @@ int columns_of(int64_t c, int ctas) { return (int)((c + 16 * ctas - 1) / (16 * c
 // needs a workspace depends on the shape alone.
 template <int R> int least_ctas(int64_t c) {
     for (int k = 1; k <= kMostCtas; k *= 2)
-        if (SmallShape<R, 8>::smem(columns_of(c, k) + 8, true) <= kMostSmem) return k;
+        if (SmallShape<R, 8>::smem(columns_of(c, k) + 8, true, k > 1) <= kMostSmem) return k;
     return 0;
 }
 int small_rows(int64_t r) { return r <= 32 ? 32 : r <= 64 ? 64 : 128; }
@@ -405,7 +421,7 @@ int small_ctas(int64_t r, int64_t c) {
 }
 
 template <typename T, int R, int WARPS, bool CLUSTER> int launch(const SmallArgs &g, int64_t batch, int ctas, cudaStream_t st) {
-    const size_t smem = SmallShape<R, WARPS>::smem(g.ldx, g.any_tail);
+    const size_t smem = SmallShape<R, WARPS>::smem(g.ldx, g.any_tail, CLUSTER);
     const cudaError_t e = cudaFuncSetAttribute(small_kernel<T, R, WARPS, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)kMostSmem);
     if (e != cudaSuccess) return cuda_status(e);
