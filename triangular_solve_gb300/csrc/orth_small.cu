@@ -14,9 +14,9 @@
 // the entries in the order of the ranks; C is computed by all of them, and C X
 // again by each for its columns.
 //
-// Measured, five steps in bf16: 1024 of 64 x 64 in 44 us, with the tensor pipe
-// 35% and the issue slots 42% busy: the latency of the matrix instructions and
-// the barriers between dependent products are what is left.
+// Measured, five steps in bf16: 1024 of 64 x 64 in 40 us, with the tensor pipe
+// 48% and the issue slots 52% busy (all matrices are in the same phase at the
+// same time, one wave of them); 1024 of 128 x 128 in 226 us.
 #include <math.h>
 #include <stdint.h>
 
@@ -71,10 +71,13 @@ template <int R, int WARPS> struct SmallShape {
     static constexpr int WM = R == 128 ? 32 : 16, WN = R == 32 ? 32 : R == 128 ? 64 : 512 / (2 * WARPS);
     static constexpr int kTiles = (R / WM) * (R / WN), kCut = WARPS / kTiles;
     static_assert(kTiles * kCut == WARPS, "a tile for each warp");
+    // Each warp has 16 whole rows of S, C and X (of 64 columns at most).
+    static constexpr bool kRows = R == 64 && WARPS == 4;
+    static constexpr int kMostColumns = 64;
     static constexpr int ld = R + 8;  // of S and C: rows 16 bytes apart in the banks
     static constexpr size_t kScratch = kCut > 1 ? (size_t)WARPS * WM * WN * 4 : 0;
     // CTAs an SM should hold
-    static constexpr int kBlocks = R == 128 ? 2 : 28 / WARPS;
+    static constexpr int kBlocks = R == 128 ? 2 : 24 / WARPS;
     static size_t smem(int ldx, bool tail, bool cluster) {
         return (size_t)R * ldx * 2 * (tail ? 2 : 1) + (cluster ? 2 : 1) * (size_t)R * ld * 2 + kScratch;
     }
@@ -101,6 +104,115 @@ __device__ __forceinline__ void tile_product(float (&acc)[WM / 16][WN / 8][4], u
             for (int j = 0; j < WN / 8; ++j) mma_f16(acc[i][j], a[i], b[j / 2][2 * (j & 1)], b[j / 2][2 * (j & 1) + 1]);
     }
 }
+
+// The products of one step where each warp has 16 whole rows of all of them:
+// what a product leaves in a warp's registers is the left factor of the next,
+// so only the right factors are read from shared memory, and C is never there.
+// The warps take the blocks of 16 columns each from its own on (a product's
+// sums over K likewise), so that a warp's rows of X are both factors at once.
+// (1024 of 64 x 64 in 40 us; with tiles through shared memory, as below, 42.)
+template <int R> struct RowsStep {
+    static constexpr int kBlocks = R / 16;
+    uint32_t xh, xl, sS;  // shared-memory addresses
+    __half *Xh, *Xl, *S;
+    int ldx, ld, strips;
+    __device__ __forceinline__ int block(int j) const { return ((int)(threadIdx.x >> 5) + j) % kBlocks; }
+
+    // alpha_s: of S; diag, beta, alpha: of C; alpha_x: of X
+    __device__ __forceinline__ void run(float alpha_s, float diag, float beta, float alpha, float alpha_x, bool split_x,
+                                        bool split_next, bool to_bf16) const {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = 16 * warp + (lane >> 2), col = (lane & 3) * 2;
+        const int brow = (lane & 7) + (lane >> 4) * 8, bcol = ((lane >> 3) & 1) * 8;  // of a right factor's rows
+        uint32_t left[kBlocks][4];
+        {  // S = X X^T
+            float acc[2 * kBlocks][4] = {};
+            for (int k = 0; k < strips; ++k) {
+                uint32_t b[kBlocks][4];
+#pragma unroll
+                for (int j = 0; j < kBlocks; ++j)
+                    ldmatrix4(b[j], xh + 2 * ((16 * block(j) + brow) * ldx + 16 * k + bcol));
+                const uint32_t a[4] = {b[0][0], b[0][2], b[0][1], b[0][3]};  // the same rows as a left factor
+#pragma unroll
+                for (int j = 0; j < 2 * kBlocks; ++j) mma_f16(acc[j], a, b[j / 2][2 * (j & 1)], b[j / 2][2 * (j & 1) + 1]);
+            }
+#pragma unroll
+            for (int j = 0; j < 2 * kBlocks; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const __half2 v = __floats2half2_rn(alpha_s * acc[j][2 * h], alpha_s * acc[j][2 * h + 1]);
+                    *reinterpret_cast<__half2 *>(S + (row + 8 * h) * ld + 16 * block(j / 2) + 8 * (j & 1) + col) = v;
+                    left[j / 2][2 * (j & 1) + h] = *reinterpret_cast<const uint32_t *>(&v);
+                }
+        }
+        __syncthreads();
+        {  // C = a I + b S + c S^2
+            float acc[2 * kBlocks][4] = {};
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k) {
+                uint32_t b[kBlocks][4];
+#pragma unroll
+                for (int j = 0; j < kBlocks; ++j)
+                    ldmatrix4(b[j], sS + 2 * ((16 * block(j) + brow) * ld + 16 * block(k) + bcol));
+#pragma unroll
+                for (int j = 0; j < 2 * kBlocks; ++j)
+                    mma_f16(acc[j], left[k], b[j / 2][2 * (j & 1)], b[j / 2][2 * (j & 1) + 1]);
+            }
+#pragma unroll
+            for (int j = 0; j < 2 * kBlocks; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t &w = left[j / 2][2 * (j & 1) + h];
+                    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                    float o0 = fmaf(beta, v.x, alpha * acc[j][2 * h]), o1 = fmaf(beta, v.y, alpha * acc[j][2 * h + 1]);
+                    if (j < 2) {  // the warp's own rows
+                        const int d = 8 * j + col - (lane >> 2) - 8 * h;
+                        o0 += d == 0 ? diag : 0.f;
+                        o1 += d == -1 ? diag : 0.f;
+                    }
+                    const __half2 c = __floats2half2_rn(o0, o1);
+                    w = *reinterpret_cast<const uint32_t *>(&c);
+                }
+        }
+        float acc[2 * SmallShape<R, R / 16>::kMostColumns / 16][4] = {};
+#pragma unroll
+        for (int i = 0; i < SmallShape<R, R / 16>::kMostColumns / 16; ++i) {
+            if (i >= strips) break;
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k) {
+                const uint32_t at = 2 * ((16 * block(k) + (lane & 15)) * ldx + 16 * i + (lane >> 4) * 8);
+                uint32_t b[4];
+                ldmatrix4_trans(b, xh + at);
+                mma_f16(acc[2 * i], left[k], b[0], b[1]);
+                mma_f16(acc[2 * i + 1], left[k], b[2], b[3]);
+                if (split_x) {
+                    ldmatrix4_trans(b, xl + at);
+                    mma_f16(acc[2 * i], left[k], b[0], b[1]);
+                    mma_f16(acc[2 * i + 1], left[k], b[2], b[3]);
+                }
+            }
+        }
+        __syncthreads();  // X has been read
+#pragma unroll
+        for (int i = 0; i < 2 * SmallShape<R, R / 16>::kMostColumns / 16; ++i) {
+            if (i >= 2 * strips) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int p = (row + 8 * h) * ldx + 8 * i + col;
+                const float o0 = alpha_x * acc[i][2 * h], o1 = alpha_x * acc[i][2 * h + 1];
+                if (to_bf16) {  // the result's bits, in X's place
+                    *reinterpret_cast<__nv_bfloat162 *>(Xh + p) = __floats2bfloat162_rn(o0, o1);
+                } else {
+                    const __half2 hi = __floats2half2_rn(o0, o1);
+                    *reinterpret_cast<__half2 *>(Xh + p) = hi;
+                    if (split_next)
+                        *reinterpret_cast<__half2 *>(Xl + p) =
+                            __floats2half2_rn(o0 - __low2float(hi), o1 - __high2float(hi));
+                }
+            }
+        }
+        __syncthreads();
+    }
+};
 
 // CLUSTER: a cluster a matrix (apart, for the registers of its sums).
 template <typename T, int R, int WARPS, bool CLUSTER>
@@ -198,12 +310,20 @@ __global__ void __launch_bounds__(32 * WARPS, CLUSTER && R == 128 ? 1 : SmallSha
     const int row = lane >> 2, col = (lane & 3) * 2;  // of a fragment's first pair; the second is 8 rows on
     for (int s = 0; s < g.steps; ++s) {
         const bool split_x = (g.tails >> s) & 1, split_next = (g.tails >> (s + 1)) & 1, last = s + 1 == g.steps;
+        const float alpha_s = kScaleS / (kScaleX * kScaleX) * (s == 0 ? rho * rho : 1.f);
+        float alpha_x = (s == 0 ? rho : 1.f) / kScaleS;
+        if (last) alpha_x /= kScaleX;
+        if constexpr (W::kRows && !CLUSTER) {
+            const RowsStep<R> step = {xh, xl, sS, Xh, Xl, S, g.ldx, W::ld, g.cp / 16};
+            step.run(alpha_s, g.coef[3 * s] * kScaleS, g.coef[3 * s + 1], g.coef[3 * s + 2] / kScaleS, alpha_x, split_x,
+                     split_next, last && g.bf16);
+            continue;
+        }
         {  // S = X X^T
             float acc[WM / 16][WN / 8][4] = {};
             const int all = g.cp / 16, each = (all + W::kCut - 1) / W::kCut;
             const int k0 = cut * each, k1 = k0 + each < all ? k0 + each : all;
             if (k0 < k1) tile_product<WM, WN>(acc, xh, g.ldx, m0, xh, g.ldx, n0, 16 * k0, k1 - k0);
-            const float alpha = kScaleS / (kScaleX * kScaleX) * (s == 0 ? rho * rho : 1.f);
             // the sums of a tile to S, or to this CTA's part of it
             float *const part = reinterpret_cast<float *>(S);  // over S and C, which are free here
             auto store = [&]() {
@@ -216,7 +336,7 @@ __global__ void __launch_bounds__(32 * WARPS, CLUSTER && R == 128 ? 1 : SmallSha
                             const int y = m0 + 16 * i + row + 8 * h, x = n0 + 8 * j + col;
                             if constexpr (!CLUSTER)
                                 *reinterpret_cast<__half2 *>(S + y * W::ld + x) =
-                                    __floats2half2_rn(alpha * acc[i][j][2 * h], alpha * acc[i][j][2 * h + 1]);
+                                    __floats2half2_rn(alpha_s * acc[i][j][2 * h], alpha_s * acc[i][j][2 * h + 1]);
                             else
                                 *reinterpret_cast<float2 *>(part + y * R + x) =
                                     make_float2(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
@@ -271,8 +391,8 @@ __global__ void __launch_bounds__(32 * WARPS, CLUSTER && R == 128 ? 1 : SmallSha
                     if (e >= share) break;
                     const int at = 4 * (rank * share + e);
                     const uint32_t to = smem_u32(S + at / R * W::ld + at % R);
-                    const __half2 lo = __floats2half2_rn(alpha * total[q].x, alpha * total[q].y);
-                    const __half2 hi = __floats2half2_rn(alpha * total[q].z, alpha * total[q].w);
+                    const __half2 lo = __floats2half2_rn(alpha_s * total[q].x, alpha_s * total[q].y);
+                    const __half2 hi = __floats2half2_rn(alpha_s * total[q].z, alpha_s * total[q].w);
                     for (int k = 0; k < ctas; ++k)
                         cluster::store_b32x2(cluster::map(to, k), *reinterpret_cast<const uint32_t *>(&lo),
                                              *reinterpret_cast<const uint32_t *>(&hi));
@@ -317,8 +437,6 @@ __global__ void __launch_bounds__(32 * WARPS, CLUSTER && R == 128 ? 1 : SmallSha
         // writes them anew, two row tiles at a time (their sums are what there
         // is to do in parallel).  Where there are fewer strips of columns than
         // warps, several warps hold a strip and share its rows.
-        float alpha = (s == 0 ? rho : 1.f) / kScaleS;
-        if (last) alpha /= kScaleX;
         constexpr int kRowTiles = R / 16, kAtOnce = R == 128 ? 1 : 2;
         const int strips = g.cp / 16;
         const int share = 2 * strips > kWarps ? 1 : min(kWarps / strips, kRowTiles / kAtOnce);
@@ -362,7 +480,7 @@ __global__ void __launch_bounds__(32 * WARPS, CLUSTER && R == 128 ? 1 : SmallSha
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int p = (16 * (i + t) + row + 8 * h) * g.ldx + j0 + 8 * j + col;
-                            const float o0 = alpha * acc[t][j][2 * h], o1 = alpha * acc[t][j][2 * h + 1];
+                            const float o0 = alpha_x * acc[t][j][2 * h], o1 = alpha_x * acc[t][j][2 * h + 1];
                             if (last && g.bf16) {  // the result's bits, in X's place
                                 *reinterpret_cast<__nv_bfloat162 *>(Xh + p) = __floats2bfloat162_rn(o0, o1);
                             } else {
