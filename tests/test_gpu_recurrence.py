@@ -186,7 +186,7 @@ def test_packed_sequences(env, name, form, lengths, D):
 # more than one step of a cluster.
 @pytest.mark.parametrize("name", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", [(1, 2500, 57), (1, 2500, 327), (1, 2500, 1025), (1, 2500, 640), (2, 1100, 1024),
-                                   (7, 600, 648)], ids=str)
+                                   (7, 600, 648), (1, 9000, 5), (40, 130, 8), (40, 130, 16), (70, 90, 24)], ids=str)
 def test_plans_of_batched_sequences(env, name, shape):
     torch, tg = env
     b, T, D = shape
@@ -199,7 +199,7 @@ def test_plans_of_batched_sequences(env, name, shape):
 
 
 @pytest.mark.parametrize("name", ["f32", "bf16"])
-@pytest.mark.parametrize("D", [57, 327, 1025, 320, 648])
+@pytest.mark.parametrize("D", [5, 8, 57, 327, 1025, 320, 648])
 def test_plans_of_packed_sequences(env, name, D):
     torch, tg = env
     c = Case(torch, name, "log", [3, 0, 2300, 40, 600], D, state=True, seed=D)

@@ -824,7 +824,9 @@ int run_layout(const LinrecArgs &a, cudaStream_t st) {
     // sequence, of packed sequences of one alone (they are few long ones as far
     // as the host knows).  Fewer lanes make more and longer stretches of few
     // units; too many for one wave of CTAs, and their narrow rows cost more than
-    // the steps that they save.  Times below are bf16, us.
+    // the steps that they save.  Lanes past the last channel are of no use at
+    // all.  Times below are bf16, us.
+    const int64_t lanes = (a.D + kVec - 1) / kVec;
     const int64_t groups = (a.D + 8 * kVec - 1) / (8 * kVec), units = PACKED ? groups : a.batch * groups;
     if (!vec) {
         // Rows off the 16-byte boundaries, 256 threads (128 are slower or no
@@ -834,9 +836,14 @@ int run_layout(const LinrecArgs &a, cudaStream_t st) {
         constexpr int kStages = BWD ? 1 : 2;
         using Wide = Plan<kVec, 8, 256, kRows, kStages, true, true, 2>;
         const bool one_step = a.T <= kMaxCluster * Wide::kStretch;
-        if (units >= 14 || one_step) return launch_scan<T, FORM, BWD, PACKED, Wide>(a, st);
-        if (units >= 5)
+        if (lanes > 4 && (units >= 14 || one_step)) return launch_scan<T, FORM, BWD, PACKED, Wide>(a, st);
+        if (lanes > 2 && (units >= 5 || one_step))
             return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 4, 256, kRows, kStages, true, true, 2>>(a, st);
+        if constexpr (kVec == 8) {
+            // (1 x 55437 x 1 forward 84 with 2 lanes, 65 with one)
+            if (lanes == 1)
+                return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 1, 256, kRows, kStages, true, true, 1>>(a, st);
+        }
         return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 2, 256, kRows, kStages, true, true, 2>>(a, st);
     }
     if constexpr (PACKED) {
@@ -851,9 +858,9 @@ int run_layout(const LinrecArgs &a, cudaStream_t st) {
         // whose lanes are half as many channels: 1 x 8192 x 1024 29, 43, 53; x
         // 512 26, 23, 35; x 256 23, 18, 18.
         constexpr bool kWide = sizeof(T) == 4;
-        if (units >= (kWide ? 20 : 64))
+        if (lanes > 4 && units >= (kWide ? 20 : 64))
             return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 8, 128, kRows, 2, false, false, 4>>(a, st);
-        if (units >= (kWide ? 10 : 20))
+        if (lanes > 2 && units >= (kWide ? 10 : 20))
             return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 4, 128, kRows, 2, false, false, 4>>(a, st);
         return launch_scan<T, FORM, BWD, PACKED, Plan<kVec, 2, 128, kRows, 2, false, false, 4>>(a, st);
     }
