@@ -26,7 +26,7 @@
 // (cp.async, so no registers and no block barrier are spent on it) and walks
 // them twice from there; they are read from memory once.  Rows that do not
 // start on 16-byte boundaries are copied as the whole 16-byte pieces that they
-// touch, and shifted into place when they are read.  A cluster of 1..8 CTAs takes consecutive stretches
+// touch, shifted into place when they are read, and written likewise.  A cluster of 1..8 CTAs takes consecutive stretches
 // of the same channels and sequence and steps along the sequence; each step
 // composes the warps' pairs in shared memory and the CTAs' pairs through
 // distributed shared memory.  There is no flag or wait in global memory, and
@@ -393,7 +393,21 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
             }
             return *reinterpret_cast<const P *>(v);
         };
-        // Stores them to their place in memory.
+        const Walk<const T> wg = walk<const T, BWD>(g.gate, seq, d);
+        const Walk<const T> wu = walk<const T, BWD>(BWD ? g.dh : g.x, seq, d);
+
+        // T is at most 2^31 - 2^16: positions past the end by two steps fit an int
+        const int step = csize * kStretch;
+        const int steps = (seq.len + step - 1) / step;
+        int base = crank * kStretch + slot * ROWS;  // this thread's first position
+        // Results to their place in memory: v are this lane's channels, p is
+        // where they go.  SHIFT in 16 bits: row r by all the lanes of the row,
+        // through staged buffer i, whose row r has been read, in whole 16-byte
+        // pieces of memory, the row's first and last in parts (1 x 65536 x 2047
+        // bf16 430 us, element by element 568: sectors written in eight goes).
+        // f32 needs four goes at most and is better off without the detour (2 x
+        // 8192 x 1001: 127, with it 141), and so is a single lane.
+        constexpr bool kPieces = L::SHIFT && sizeof(T) == 2 && LANES > 1;
         auto put = [&](T *p, const P &v) {
             if constexpr (!L::SHIFT) {
                 store_pack<T, VEC>(p, v);
@@ -406,13 +420,35 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
                     if (d + k < g.D) p[k] = v.v[k];
             }
         };
-        const Walk<const T> wg = walk<const T, BWD>(g.gate, seq, d);
-        const Walk<const T> wu = walk<const T, BWD>(BWD ? g.dh : g.x, seq, d);
-
-        // T is at most 2^31 - 2^16: positions past the end by two steps fit an int
-        const int step = csize * kStretch;
-        const int steps = (seq.len + step - 1) / step;
-        int base = crank * kStretch + slot * ROWS;  // this thread's first position
+        auto put_pieces = [&](T *p, const P &v, int r, int i) {
+            if constexpr (kPieces) {
+                unsigned char *const row = staged_row(i, r) + 16;
+                __syncwarp();
+                if (base + r < len) *reinterpret_cast<P *>(row + col * 16) = v;
+                __syncwarp();
+                if (base + r >= copy_len) return;
+                const uint32_t shift = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u;
+                // elements that the row's first piece holds before it, and of this CTA's row
+                const int before = (int)(shift / sizeof(T)), n = (int)min((int64_t)kChannels, g.D - c0);
+                const int first = col * VEC - before;  // of this lane's piece
+                if (first >= 0) {
+                    const P piece = own(i, r, 16u - shift);
+                    if (first + VEC <= n) {
+                        store_pack<T, VEC>(p - before, piece);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < VEC; ++k)
+                            if (first + k < n) p[k - before] = piece.v[k];
+                    }
+                }
+                if (before) {
+                    for (int k = col; k < VEC; k += LANES) {
+                        const int at = k >= before ? k - before : kChannels - before + k;
+                        if (at < n) p[at - col * VEC] = reinterpret_cast<const T *>(row)[at];
+                    }
+                }
+            }
+        };
         // the next step's gate and x (dh) into buffer pair `i`
         auto stage_next = [&](int at, int i) {
             stage(wg, g.gate, at, copy_len, 2 * i);
@@ -575,8 +611,9 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
                 T *out = wo.at + base * wo.step;
 #pragma unroll
                 for (int r = 0; r < ROWS; ++r) {
+                    P o;
                     if (base + r < len) {
-                        P o, q, e;
+                        P q, e;
                         if constexpr (!kKeep) {
                             q = own(bg, r, (shift_g + r * next_g) & 15u);
                             e = own(bu, r, (shift_u + r * next_u) & 15u);
@@ -595,8 +632,9 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
                             h[k] = mad_(at, h[k], ut);
                             set_value(o, k, h[k]);
                         }
-                        put(out + r * wo.step, o);
+                        if constexpr (!kPieces) put(out + r * wo.step, o);
                     }
+                    put_pieces(out + r * wo.step, o, r, bg);
                 }
             } else {
                 const Walk<T> wo = walk<T, BWD>(g.dgate, seq, d), wx = walk<T, BWD>(g.dx, seq, d);
@@ -614,9 +652,10 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
                 }
 #pragma unroll
                 for (int r = 0; r < ROWS; ++r) {
+                    P o0, o1;
                     if (base + r < len) {
                         const P q = own(bg, r, (shift_g + r * next_g) & 15u), e = own(bu, r, (shift_u + r * next_u) & 15u);
-                        P o0, o1, before, in;
+                        P before, in;
                         if constexpr (L::SIDE) {
                             before = own(2 * L::STAGES, r, (shift_h + r * next_h) & 15u);
                             if constexpr (kSigmoid) in = own(2 * L::STAGES + 1, r, (shift_x + r * next_x) & 15u);
@@ -650,9 +689,13 @@ __global__ void __launch_bounds__(L::kThreads, L::kBlocks)
                                 set_value(o1, k, mul_(full, rest));
                             }
                         }
-                        put(og + r * wo.step, o0);
-                        put(ox + r * wx.step, o1);
+                        if constexpr (!kPieces) {
+                            put(og + r * wo.step, o0);
+                            put(ox + r * wx.step, o1);
+                        }
                     }
+                    put_pieces(og + r * wo.step, o0, r, bg);
+                    put_pieces(ox + r * wx.step, o1, r, bu);
                 }
             }
             if constexpr (L::SHIFT) __syncwarp();
@@ -832,7 +875,8 @@ int run_layout(const LinrecArgs &a, cudaStream_t st) {
         // Rows off the 16-byte boundaries, 256 threads (128 are slower or no
         // faster) of 8, 4, 2 lanes: forward 1 x 65536 x 2047 569, 635, 1170;
         // backward 1 x 28672 x 429 279, 164, 219; forward 1 x 32768 x 221 packed
-        // 217, 121, 86.
+        // 217, 121, 86 (all with results stored element by element; in pieces,
+        // as now, the ones chosen take 430, 141, 78).
         constexpr int kStages = BWD ? 1 : 2;
         using Wide = Plan<kVec, 8, 256, kRows, kStages, true, true, 2>;
         const bool one_step = a.T <= kMaxCluster * Wide::kStretch;
